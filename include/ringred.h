@@ -406,6 +406,111 @@ rr_status ring_selftest_bounded_wait(unsigned long long limit_ns, cudaStream_t s
 int ring_debug_checks(void);
 rr_status ring_debug_set_margin(size_t bytes);
 
+/*
+ * Microscaled 4-bit matrices.  Beside the 16-bit wire, gradients and the
+ * operands of training and serving products can be held in 4 bits: 32
+ * neighbours along a row are a block with one scale 2^X (a byte, X + 127), an
+ * element is a sign and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 times the scale.
+ *   X is the smallest integer >= -127 with max|x| <= 6 * 2^X over the block
+ *   (nothing is clipped); the last block of a row may be short.
+ *   RR_MX4_NEAREST: the nearest value, ties to the even one of the two.
+ *   RR_MX4_STOCHASTIC: with f the way from the value below |x| / 2^X to the
+ *   one above, the one above if floor(f * 2^16) + u >= 2^16 for the element's
+ *   16-bit random number u: unbiased to 2^-16 of a step.
+ *   A block that holds an infinity or a NaN has scale byte 255 and reads as
+ *   NaN throughout.
+ *
+ * Random numbers (here and in dropout) are Philox4x32-10 (Salmon, Moraes,
+ * Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011) with key
+ * `seed` and counter (i / 8, subsequence): its 128 bits are the 16-bit numbers
+ * of elements i .. i + 7, low halves first.  They depend on the element, not
+ * on the launch, so nothing random is ever stored and any piece of a tensor
+ * can be computed by itself.
+ *
+ * Storage of a rows x cols matrix: data, rows of ring_mx4_row_bytes(cols)
+ * bytes (16 per block), two elements a byte, the lower one in the low half,
+ * zeros past the last column; scales, ring_mx4_scale_bytes(rows, cols) bytes
+ * in tiles of 128 rows by 8 blocks (row-major), the byte of row r and block j
+ * at ((r / 128) * ceil(cols / 256) + j / 8) * 1024 + (j / 4 % 2) * 512 +
+ * (r % 32) * 16 + (r / 32 % 4) * 4 + j % 4, zeros where there is no block.
+ * Both are device memory, 16-byte aligned, owned by the caller.
+ *
+ * The calls below follow the common rules above (asynchronous on `stream`,
+ * arguments checked first, no allocation, programmatic launch); matrices are
+ * row-major with ld >= cols elements from row to row (any ld and any
+ * element-aligned address; 16-byte aligned rows are the fast path).  rows or
+ * cols of zero: RR_OK, nothing is done.  rows and cols are below 2^31 - 256.
+ * The debug build's bounds checks do not cover them.
+ */
+typedef struct {
+  void *data;
+  void *scales;
+  size_t rows, cols;
+} rr_mx4;
+
+typedef enum { RR_MX4_NEAREST = 0, RR_MX4_STOCHASTIC = 1 } rr_mx4_rounding;
+
+size_t ring_mx4_row_bytes(size_t cols);
+size_t ring_mx4_scale_bytes(size_t rows, size_t cols);
+
+/*
+ * Dropout: element i = first + row * cols + column of a tensor is kept if its
+ * 16-bit random number is at least T = round(65536 p) and is then multiplied
+ * by 65536 / (65536 - T) (so the mean is exact for the T in use); it is 0
+ * otherwise, whatever it held.  0 <= p, T < 65536.  `first` places a shard or
+ * a range inside the whole tensor.
+ */
+typedef struct {
+  double p;
+  unsigned long long seed, subsequence, first;
+} rr_dropout;
+
+/*
+ * ring_dropout -- out = (residual +) dropout(x); with x a gradient and no
+ * residual it is dropout's own backward pass.  residual may be NULL.  Sums in
+ * binary32, one rounding to storage.  out may be x or residual (same address
+ * and ld); any other overlap is RR_ERR_ALIAS.
+ */
+rr_status ring_dropout(const void *x, size_t ld_x, const void *residual, size_t ld_residual, void *out, size_t ld_out,
+                       size_t rows, size_t cols, rr_dtype dtype, const rr_dropout *drop, cudaStream_t stream);
+
+/*
+ * ring_mx4_quantize -- a rows x cols matrix to 4 bits, along its rows
+ * (by_rows: rows x cols), its columns (by_cols: cols x rows, the transpose
+ * quantised along its own rows), or both in one pass over x; NULL for what is
+ * not wanted.  drop, if not NULL: x is dropped out first, in binary32 and
+ * unrounded (the gradient of a dropped-out product goes to 4 bits without ever
+ * being stored).  seed and subsequence: the numbers of stochastic rounding,
+ * element (r, k) of the result at i = r * 32 * ceil(K / 32) + k for a result
+ * with K columns; by_cols takes subsequence + 1 when both are wanted.
+ */
+rr_status ring_mx4_quantize(const void *x, size_t rows, size_t cols, size_t ld, rr_dtype dtype, const rr_mx4 *by_rows,
+                            const rr_mx4 *by_cols, rr_mx4_rounding rounding, unsigned long long seed,
+                            unsigned long long subsequence, const rr_dropout *drop, cudaStream_t stream);
+
+/* ring_mx4_dequantize -- the values of a 4-bit matrix, rounded to dtype (4 and
+ * 6 times 2^126 lie above binary32 and become infinity). */
+rr_status ring_mx4_dequantize(const rr_mx4 *q, void *out, size_t ld, rr_dtype dtype, cudaStream_t stream);
+
+/*
+ * ring_mx4_matmul -- out[i][j] = (residual[i][j] +) dropout(sum_k a[i][k] *
+ * b[j][k]): the product of two 4-bit matrices with equal cols, both held along
+ * the summed axis, on the block-scaled tensor cores; sums in binary32, one
+ * rounding to storage.  out: a->rows x b->rows.  residual and drop may be
+ * NULL; residual may be out itself.  With cols of zero the sum is 0.
+ */
+rr_status ring_mx4_matmul(const rr_mx4 *a, const rr_mx4 *b, void *out, size_t ld, rr_dtype dtype, const void *residual,
+                          size_t ld_residual, const rr_dropout *drop, cudaStream_t stream);
+
+/*
+ * ring_mx4_allreduce -- the AllReduce of R equal matrices on a 4-bit wire:
+ * every out_bufs[r] (rows * cols elements, contiguous) receives the flat
+ * ring's fold of the R matrices' values, in binary32, element i = row * cols +
+ * column starting at the rank of its chunk, rounded once to dtype: bit for bit
+ * ring_allreduce_ex of the values with a binary32 wire.  in: R descriptors.
+ */
+rr_status ring_mx4_allreduce(const rr_mx4 *in, void *const *out_bufs, int R, rr_dtype dtype, cudaStream_t stream);
+
 /* RR_ABI_VERSION of the library. */
 int ring_abi_version(void);
 

@@ -14,11 +14,17 @@ from typing import Optional, Sequence
 
 import torch
 
+from . import mx4 as _mx4
+from .mx4 import (Dropout, Mx4, dropout, mx4_allreduce, mx4_dequantize, mx4_linear, mx4_matmul, mx4_quantize,
+                  mx4_quantize_both)
+
 __all__ = [
     "RingError", "lib", "allreduce", "reduce_scatter", "allgather", "collective", "plan",
     "allreduce_range", "allreduce_host", "allreduce_host_static", "host_workspace_bytes", "allreduce_algo",
     "chunk_count", "chunk_offset", "device_status", "selftest_bounded_wait", "LaunchCfg", "rank_buffers",
     "debug_checks", "debug_set_margin", "HOST_COPIES_OVERLAP", "HOST_COPIES_ONE_WAY",
+    "Mx4", "Dropout", "mx4_quantize", "mx4_quantize_both", "mx4_dequantize", "mx4_matmul", "mx4_allreduce",
+    "mx4_linear", "dropout",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_ALIAS", "ERR_CUDA", "ERR_TIMEOUT",
     "OP_ALLREDUCE", "OP_REDUCE_SCATTER", "OP_ALLGATHER", "PATH_AUTO", "PATH_BULK", "PATH_SIMPLE", "PATH_DIRECT",
 ]
@@ -143,6 +149,7 @@ def lib() -> ctypes.CDLL:
         L.ring_debug_checks.restype = i
         L.ring_debug_set_margin.argtypes = [sz]
         L.ring_debug_set_margin.restype = i
+        _mx4.bind(L)
         _lib = L
     return _lib
 

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "ringred.h"
+#include "rr_mx4.h"
 #include "rr_params.h"
 
 namespace {
@@ -852,6 +853,20 @@ rr_status static_scratch_for_current_device(unsigned char **out) {
 }
 
 }  // namespace
+
+namespace rr {
+
+rr_status device_info(unsigned int **status, int *sms) {
+  DeviceInfo dev;
+  const rr_status st = current_device(&dev);
+  if (st != RR_OK) return st;
+  *status = dev.status, *sms = dev.sms;
+  return RR_OK;
+}
+
+bool note_cuda(cudaError_t e) { return cuda_ok(e); }
+
+}  // namespace rr
 
 extern "C" {
 

@@ -1,0 +1,108 @@
+// rr_mx4.h -- parameter blocks and launchers of the microscaled 4-bit
+// operators and dropout, between the C ABI (rr_mx4_api.cu) and the kernel
+// translation units (rr_mx4_convert.cu, rr_mx4_matmul.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "ringred.h"
+#include "rr_params.h"
+
+namespace rr {
+
+// A block is 32 elements under one scale byte; the scales of 128 rows by
+// 8 blocks (256 elements) are one tile of 1024 bytes, in the order the tensor
+// cores' scale copies read: two atoms of 512 bytes (4 blocks each), where row
+// r of the 128 has 4 bytes at (r % 32) * 16 + (r / 32) * 4.
+constexpr int kMx4Block = 32;
+constexpr int kMx4TileRows = 128;
+constexpr int kMx4TileCols = 256;
+constexpr int kMx4TileBytes = 1024;
+constexpr int kMx4AtomBytes = 512;
+
+template <class T>
+__host__ __device__ constexpr T ceil_div(T a, T b) {
+  return (a + b - 1) / b;
+}
+
+struct Mx4Out {
+  uint8_t *data;         // [rows][row_bytes]
+  uint8_t *scales;       // [ceil(rows / 128)][tiles_k][1024]
+  long long rows;
+  long long row_bytes;   // 16 * ceil(cols / 32)
+  long long tiles_k;     // ceil(cols / 256)
+};
+
+struct DropParams {
+  unsigned long long seed, subsequence, first;
+  unsigned int threshold;  // kept if the 16-bit number is at least this; 0: everything is kept
+  float scale;             // 65536 / (65536 - threshold)
+};
+
+struct QuantParams {
+  const void *x;
+  long long rows, cols, ld;
+  Mx4Out by_rows, by_cols;   // data null: not wanted
+  unsigned long long seed, subsequence;  // stochastic rounding (by_cols: subsequence + 1 if both are wanted)
+  DropParams drop;
+  int dtype;
+  bool stochastic;
+  bool vec;   // every 16-byte group of a row is aligned
+};
+
+struct DequantParams {
+  const uint8_t *data, *scales;
+  long long rows, cols, row_bytes, tiles_k;
+  void *out;
+  long long ld;
+  int dtype;
+  bool vec;
+};
+
+struct DropoutParams {
+  const void *x, *residual;  // residual may be null
+  void *out;
+  long long rows, cols, ld_x, ld_res, ld_out;
+  DropParams drop;
+  int dtype;
+  bool vec;
+};
+
+struct Mx4ReduceParams {
+  const uint8_t *data[RR_MAX_RANKS], *scales[RR_MAX_RANKS];
+  void *out[RR_MAX_RANKS];
+  long long rows, cols, row_bytes, tiles_k, base;  // base: floor(rows * cols / R)
+  int R, dtype;
+  bool vec;
+};
+
+struct Mx4Operand {
+  const uint8_t *data, *scales;
+  long long rows, row_bytes;
+};
+
+struct MatmulParams {
+  Mx4Operand a, b;
+  long long m, n, k;
+  void *out;
+  const void *residual;   // may be null
+  long long ld_out, ld_res;
+  DropParams drop;
+  unsigned int *status;
+  int dtype, sms;
+  bool vec;  // every 16-byte group of the rows of out and residual is aligned
+};
+
+cudaError_t launch_mx4_quantize(const QuantParams &p, cudaStream_t s);
+cudaError_t launch_mx4_dequantize(const DequantParams &p, cudaStream_t s);
+cudaError_t launch_dropout(const DropoutParams &p, cudaStream_t s);
+cudaError_t launch_mx4_reduce(const Mx4ReduceParams &p, cudaStream_t s);
+cudaError_t launch_mx4_matmul(const MatmulParams &p, cudaStream_t s);
+
+// Defined in rr_api.cu: the current device's status word and SM count, and the
+// record behind ring_last_cuda_error.
+rr_status device_info(unsigned int **status, int *sms);
+bool note_cuda(cudaError_t e);
+
+}  // namespace rr

@@ -1,0 +1,119 @@
+// rr_tcgen05.cuh -- PTX wrappers of the fifth-generation tensor cores
+// (tcgen05: tensor memory, block-scaled products, scale copies) and of tiled
+// tensor copies, for the microscaled 4-bit product.
+#pragma once
+
+#include <cuda.h>
+
+#include "rr_device.cuh"
+
+namespace rr {
+
+// --------------------------------------------------------------------------
+// tensor memory
+// --------------------------------------------------------------------------
+
+// Whole warp.  Writes the address of `columns` (a power of two, 32 .. 512)
+// fresh columns to *slot.
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns) : "memory");
+}
+
+__device__ __forceinline__ void tcgen05_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tcgen05_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Arrives on `bar` when every tensor operation this thread issued has completed.
+__device__ __forceinline__ void tcgen05_commit(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+
+// 32 lanes (this warp's quarter) by 32 columns of accumulators.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t r[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// --------------------------------------------------------------------------
+// shared-memory matrix descriptors: bits 0-13 start / 16, 16-29 leading-dimension
+// byte offset / 16, 32-45 stride byte offset / 16, 46-47 version (1), 61-63 swizzle
+// --------------------------------------------------------------------------
+
+// A K-major operand tile of 128-byte rows with the 128-byte swizzle: groups of
+// eight rows are 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t smem) {
+  return (uint64_t)((smem >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// An unswizzled column of 16-byte rows (one scale atom: 32 rows): groups of
+// eight rows are 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem) {
+  return (uint64_t)((smem >> 4) & 0x3fff) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+}
+
+// One scale atom (128 rows by 4 blocks, 512 bytes) to four columns of tensor
+// memory, the same in the lanes of all four warps.
+__device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// Instruction descriptor of a block-scaled 4-bit product (E2M1 by E2M1 with
+// E8M0 scales, both operands K-major): bits 4-5 / 29-30 the first scale byte
+// of B / A in each 32-bit column (0 or 2), 7-9 and 10-11 the element formats
+// (1: E2M1), 17-22 N / 8, 23 the scale format (1: E8M0), 27-28 M / 128.
+__device__ __forceinline__ constexpr uint32_t mx4_instr_desc(int M, int N, int scale_at) {
+  return ((uint32_t)scale_at << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(M >> 7) << 27) | ((uint32_t)scale_at << 29);
+}
+
+// D += A B^T over 64 elements of K (two scale blocks); accumulate false: D = A B^T.
+__device__ __forceinline__ void mx4_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t scale_a,
+                                        uint32_t scale_b, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// --------------------------------------------------------------------------
+// tiled tensor copies
+// --------------------------------------------------------------------------
+
+// Box of the two-dimensional map at (x bytes, row y); x is a multiple of 16.
+__device__ __forceinline__ void tensor_load(void *smem_dst, const CUtensorMap *map, int x, int y, uint64_t *bar,
+                                            uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(smem_dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar)), "l"(pol)
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+__device__ __forceinline__ uint64_t l2_evict_last_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+__device__ __forceinline__ uint64_t l2_evict_normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+}  // namespace rr

@@ -133,6 +133,13 @@ __device__ __forceinline__ void store8(void *base, long long at, int valid, bool
   }
 }
 
+// 32 bytes to a 32-byte aligned address: a whole sector from one thread.
+__device__ __forceinline__ void stg32(void *p, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // v[j] *= scale where element i + j is kept, 0 where it is dropped.
 __device__ __forceinline__ void drop8(const DropParams &d, unsigned long long i, float v[8]) {
   const uint4 u = numbers8(d.seed, d.subsequence, d.first + i);

@@ -91,7 +91,8 @@ struct MatmulParams {
   DropParams drop;
   unsigned int *status;
   int dtype, sms;
-  bool vec;  // every 16-byte group of the rows of out and residual is aligned
+  bool vec;    // every 16-byte group of the rows of out and residual is aligned
+  bool vec32;  // every 32-byte group of the rows of out
 };
 
 cudaError_t launch_mx4_quantize(const QuantParams &p, cudaStream_t s);

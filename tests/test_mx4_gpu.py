@@ -249,7 +249,8 @@ def product_bound(a, b, y, dtype):
 
 PRODUCTS = [(1, 1, 1), (1, 8, 32), (1, 300, 64), (2, 129, 65), (7, 16, 4096), (16, 128, 256), (17, 127, 257),
             (33, 512, 1000), (64, 130, 2000), (127, 64, 511), (128, 128, 128), (129, 200, 768), (200, 333, 1537),
-            (256, 256, 512), (300, 520, 300), (513, 257, 1030)]
+            (256, 256, 512), (300, 520, 300), (513, 257, 1030),
+            (2561, 2050, 300), (1111, 5000, 1030), (130, 19_500, 65)]
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
@@ -266,7 +267,7 @@ def test_product(rr, m, n, k, dtype):
     assert torch.equal(out, rr.mx4_matmul(qa, qb, dtype)), "two calls differ"
 
 
-@pytest.mark.parametrize("m,n,k", [(3, 40, 64), (130, 260, 300), (300, 1000, 512)])
+@pytest.mark.parametrize("m,n,k", [(3, 40, 64), (130, 260, 300), (300, 1000, 512), (2500, 2300, 1600)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_product_places_every_element(rr, m, n, k, dtype):
     """Sums of one term each: out[i, j] is exact, so any mix-up of rows, columns, K or scales shows."""
@@ -284,7 +285,8 @@ def test_product_places_every_element(rr, m, n, k, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
-@pytest.mark.parametrize("m,n,k,p", [(1, 40, 64, 0.0), (5, 33, 96, 0.2), (130, 129, 256, 0.1), (300, 264, 512, 0.5)])
+@pytest.mark.parametrize("m,n,k,p", [(1, 40, 64, 0.0), (5, 33, 96, 0.2), (130, 129, 256, 0.1), (300, 264, 512, 0.5),
+                                     (2600, 2050, 320, 0.1), (2304, 2560, 64, 0.3)])
 def test_product_epilogue(rr, m, n, k, p, dtype):
     """residual + dropout(product): the elements of the plain product in binary32, masked and added."""
     da, sa, _ = ref.random_matrix(m, k, 1, spread=1)

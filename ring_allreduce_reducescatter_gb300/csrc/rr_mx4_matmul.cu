@@ -8,25 +8,20 @@ namespace rr {
 
 namespace {
 
-// Tile of a CTA: 128 rows of A by kBN rows of B, K in steps of 256 elements
-// (128 bytes a row, one scale tile).
-constexpr int kBM = 128, kBN = 128, kBK = 256;
-constexpr int kStages = 6;
+// K goes in steps of 256 elements: 128 bytes a row, one scale tile.
+constexpr int kBK = 256;
 constexpr int kRowBytes = kBK / 2;
-constexpr int kStageA = kBM * kRowBytes, kStageB = kBN * kRowBytes;
-constexpr int kStageBytes = kStageA + kStageB + 2 * kMx4TileBytes;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-constexpr int kMatmulThreads = 192;  // warps 0-3 epilogue, 4 copies, 5 products
-constexpr uint32_t kTmemColumns = 256;  // kBN accumulators, then the scales of two steps
-constexpr uint32_t kTmemScales = kBN;
+constexpr int kHalfBytes = 128 * kRowBytes;  // 128 rows of an operand, one step
 
 struct MatmulKernelParams {
-  CUtensorMap map_a, map_b;
-  CUtensorMap map_sa, map_sb;  // the scale tiles, 8 rows of 128 bytes each (pair kernel)
-  const uint8_t *scales_a, *scales_b;
+  // the operands by their sides of the tensor cores' product: P gives the rows
+  // of the accumulators, Q the columns
+  CUtensorMap map_p, map_q;
+  CUtensorMap map_sp, map_sq;  // their scale tiles, 8 rows of 128 bytes each (pair kernel)
+  const uint8_t *scales_p, *scales_q;
   long long m, n;
   int steps;  // of K
-  int tiles_m, tiles_n;
+  int tiles_p, tiles_q;
   void *out;
   const void *residual;
   long long ld_out, ld_res;
@@ -35,140 +30,353 @@ struct MatmulKernelParams {
   bool vec, vec32;  // 16- and 32-byte groups of the rows of out (and residual, for vec) are aligned
 };
 
-// Sixteen accumulators of one row, from column `col` on, to the output.
-template <int DT>
-__device__ __forceinline__ void finish16(const MatmulKernelParams &p, long long row, long long col,
-                                         const uint32_t *acc) {
-  const long long left = p.n - col;
-  if (row >= p.m || left <= 0) return;
-  float v[16];
+// Masks kN accumulators of one row, from column `col` on.
+template <int kN>
+__device__ __forceinline__ void drop_row(const MatmulKernelParams &p, long long row, long long col, float v[kN]) {
+  const unsigned long long i = p.drop.first + (unsigned long long)(row * p.n + col), g = i >> 3;
+  const int sh = (int)(i & 7) * 2;
+  uint4 u = philox(p.drop.seed, p.drop.subsequence, g);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(acc[j]);
+  for (int h = 0; h < kN / 8; ++h) {
+    const uint4 next = sh == 0 && h + 1 == kN / 8 ? u : philox(p.drop.seed, p.drop.subsequence, g + h + 1);
+    const uint4 w = sh == 0 ? u : funnel16(u, next, sh);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int valid = (int)min(8ll, left - 8 * h);
-    if (valid <= 0) break;
-    if (p.drop.threshold) drop8(p.drop, (unsigned long long)(row * p.n + col + 8 * h), v + 8 * h);
-    if (p.residual) {
+    for (int j = 0; j < 8; ++j)
+      v[8 * h + j] = number_of(w, j) >= p.drop.threshold ? __fmul_rn(v[8 * h + j], p.drop.scale) : 0.f;
+    u = next;
+  }
+}
+
+// A warp's 32 rows of kN accumulators each, a row a lane, to the output.
+// rows0, col: the block's first row and column; res: the lane's part of the
+// residual, loaded ahead by load_residual (aligned blocks only).
+// stage: kStageFloats of shared memory of this warp's own.
+constexpr int kStageFloats = 32 * 17;
+
+// Whether a block of kN columns takes the vector path.
+template <int kN>
+__device__ __forceinline__ bool aligned_block(const MatmulKernelParams &p, long long col) {
+  return p.vec && col + kN <= p.n;
+}
+template <int DT, int kN>
+__device__ __forceinline__ void load_residual(const MatmulKernelParams &p, long long row, long long col, uint4 *res) {
+  using T = typename Fmt<DT>::type;
+  const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.residual) + row * p.ld_res + col);
+#pragma unroll
+  for (int j = 0; j < kN / 8 * kRaw8<DT>; ++j) res[j] = row < p.m ? ldg_l1(q + j) : make_uint4(0, 0, 0, 0);
+}
+
+template <int DT, int kN>
+__device__ __forceinline__ void finish_aligned(const MatmulKernelParams &p, long long row, long long col,
+                                               const uint32_t *acc, const uint4 *res) {
+  using T = typename Fmt<DT>::type;
+  if (row >= p.m) return;
+  float v[kN];
+#pragma unroll
+  for (int j = 0; j < kN; ++j) v[j] = __uint_as_float(acc[j]);
+  if (p.drop.threshold) drop_row<kN>(p, row, col, v);
+  if (p.residual) {
+#pragma unroll
+    for (int h = 0; h < kN / 8; ++h) {
       float w[8];
-      load8<DT>(p.residual, row * p.ld_res + col + 8 * h, valid, p.vec, w);
+      widen8<DT>(res + h * kRaw8<DT>, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[8 * h + j] = __fadd_rn(w[j], v[8 * h + j]);
     }
   }
-  if (p.vec32 && left >= 16) {
-    using T = typename Fmt<DT>::type;
-    T *o = static_cast<T *>(p.out) + row * p.ld_out + col;
-    uint4 raw[2 * kRaw8<DT>];
-    narrow8<DT>(v, raw), narrow8<DT>(v + 8, raw + kRaw8<DT>);
+  uint4 raw[kN / 8 * kRaw8<DT>];
 #pragma unroll
-    for (int j = 0; j < kRaw8<DT>; ++j) stg32(reinterpret_cast<uint4 *>(o) + 2 * j, raw[2 * j], raw[2 * j + 1]);
-  } else {
-    store8<DT>(p.out, row * p.ld_out + col, (int)min(8ll, left), p.vec, v);
-    if (left > 8) store8<DT>(p.out, row * p.ld_out + col + 8, (int)min(8ll, left - 8), p.vec, v + 8);
+  for (int h = 0; h < kN / 8; ++h) narrow8<DT>(v + 8 * h, raw + h * kRaw8<DT>);
+  uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + row * p.ld_out + col);
+#pragma unroll
+  for (int j = 0; j < kN / 8 * kRaw8<DT>; j += 2) {
+    if (p.vec32) {
+      stg32(o + j, raw[j], raw[j + 1]);
+    } else {
+      stg_stream(o + j, raw[j]);
+      stg_stream(o + j + 1, raw[j + 1]);
+    }
   }
 }
 
+// Sixteen columns of a block whose rows are not aligned, or end inside it: the
+// block is turned in shared memory so that sixteen lanes take neighbours of a row
+// (a lane storing its own row by single elements made such products twice as long).
 template <int DT>
-__global__ void __launch_bounds__(kMatmulThreads, 1) mx4_matmul_kernel(const __grid_constant__ MatmulKernelParams p) {
+__device__ __forceinline__ void finish_ragged(const MatmulKernelParams &p, long long rows0, long long col,
+                                              const uint32_t *acc, float *stage) {
+  using T = typename Fmt<DT>::type;
+  const int lane = threadIdx.x % 32;
+  if (col >= p.n || rows0 >= p.m) return;  // the same for the whole warp
+  float v[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(acc[j]);
+  if (p.drop.threshold) drop_row<16>(p, rows0 + lane, col, v);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = v[j];
+  __syncwarp();
+  const long long c = col + lane % 16, r0 = rows0 + lane / 16;
+  const bool in = c < p.n;
+  float w[16];
+  if (p.residual) {
+    const T *q = static_cast<const T *>(p.residual) + r0 * p.ld_res + c;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w[k] = in && r0 + 2 * k < p.m ? to_f32<DT>(q[2 * k * p.ld_res]) : 0.f;
+  }
+  T *o = static_cast<T *>(p.out) + r0 * p.ld_out + c;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    float x = stage[(2 * k + lane / 16) * 17 + lane % 16];
+    if (p.residual) x = __fadd_rn(w[k], x);
+    if (in && r0 + 2 * k < p.m) o[2 * k * p.ld_out] = from_f32<DT>(x);
+  }
+  __syncwarp();
+}
+
+template <int DT>
+__device__ __forceinline__ void finish16(const MatmulKernelParams &p, long long row, long long col, const uint32_t *acc,
+                                         float *stage) {
+  if (aligned_block<16>(p, col)) {
+    uint4 res[2 * kRaw8<DT>];
+    if (p.residual) load_residual<DT, 16>(p, row, col, res);
+    finish_aligned<DT, 16>(p, row, col, acc, res);
+  } else {
+    finish_ragged<DT>(p, row - threadIdx.x % 32, col, acc, stage);
+  }
+}
+
+// One accumulator to the output (the element's own random number: a whole
+// counter for one element, for the few columns of a small batch).
+template <int DT>
+__device__ __forceinline__ void finish1(const MatmulKernelParams &p, long long row, long long col, float v) {
+  using T = typename Fmt<DT>::type;
+  if (row >= p.m || col >= p.n) return;
+  if (p.drop.threshold) {
+    const unsigned long long i = p.drop.first + (unsigned long long)(row * p.n + col);
+    const uint4 u = philox(p.drop.seed, p.drop.subsequence, i >> 3);
+    v = number_of(u, (int)(i & 7)) >= p.drop.threshold ? __fmul_rn(v, p.drop.scale) : 0.f;
+  }
+  if (p.residual) v = __fadd_rn(to_f32<DT>(static_cast<const T *>(p.residual)[row * p.ld_res + col]), v);
+  static_cast<T *>(p.out)[row * p.ld_out + col] = from_f32<DT>(v);
+}
+
+// --------------------------------------------------------------------------
+// small products: K split over a cluster
+// --------------------------------------------------------------------------
+
+// A cluster of S CTAs computes one tile of 128 rows of P by BN rows of Q, each
+// CTA a contiguous part of K; the parts meet in shared memory, where CTA r adds
+// its share of the columns over all CTAs in rank order (so the result does not
+// depend on timing) and finishes it.  Reading the operands bounds these
+// products, and a grid of whole tiles would leave most SMs without a share of
+// the memory; S is the largest split that still fits the GPU at two CTAs an SM.
+// kSwap: P is B (a weight matrix, 128 rows a tile) and Q is A (the few tokens
+// of a small batch, BN of them): no operand row is padded beyond BN tokens.
+constexpr int kSplitThreads = 192;  // warps 0-3 epilogue, 4 copies, 5 products
+
+template <int BN>
+struct Split {
+  static constexpr int kStageBytes = kHalfBytes + BN * kRowBytes + 2 * kMx4TileBytes;
+  static constexpr int kStages = BN <= 32 ? 5 : BN == 64 ? 4 : 3;  // about 104 KB: two CTAs an SM
+  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+  static constexpr uint32_t kScales = BN;                          // first column of the scales
+  static constexpr uint32_t kColumns = BN <= 64 ? 128 : 256;       // accumulators and the scales of every stage
+  static_assert(kScales + kStages * 16 <= kColumns, "they fit");
+  static_assert(kStages * kStageBytes >= 128 * BN * 4 + 4 * kStageFloats * 4, "a part of a tile fits the stages");
+};
+
+// The sums over the S parts of kV neighbouring columns of this thread's row,
+// kN groups of them, from column c on: every load is issued before the first
+// sum, since another CTA's shared memory is about a microsecond away.
+template <int S, int kV, int kN>
+__device__ __forceinline__ void add_parts(const float *part, int c, int row, float v[kN * kV]) {
+  float4 w[S][kN];
+#pragma unroll
+  for (int r = 0; r < S; ++r)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      // columns 4 g .. 4 g + 3 of a row are 16 bytes, rows follow one another
+      const int col = c + n * kV;
+      const uint32_t at = cluster_addr(part + (col / 4 * 128 + row) * 4 + col % 4, r);
+      w[r][n] = kV == 4 ? cluster_load4(at) : cluster_load2(at);
+    }
+#pragma unroll
+  for (int n = 0; n < kN; ++n) {
+#pragma unroll
+    for (int r = 0; r < S; ++r) {
+      const float *x = &w[r][n].x;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v[n * kV + j] = r == 0 ? x[j] : __fadd_rn(v[n * kV + j], x[j]);
+    }
+  }
+}
+
+// This CTA's share of the columns of a split tile, added up and finished.
+template <int DT, int BN, bool kSwap, int S>
+__device__ __forceinline__ void finish_split(const MatmulKernelParams &p, const float *part, int rank, int row,
+                                             long long prow, long long q0, float *stage) {
+  constexpr int kShare = BN / S;
+  const int c0 = rank * kShare;
+  if constexpr (kSwap) {
+    constexpr int kV = kShare < 4 ? 2 : 4, kN = kShare / kV < 4 ? kShare / kV : 4;
+#pragma unroll 1
+    for (int c = c0; c < c0 + kShare && q0 + c < p.m; c += kN * kV) {
+      float v[kN * kV];
+      add_parts<S, kV, kN>(part, c, row, v);
+#pragma unroll
+      for (int j = 0; j < kN * kV; ++j) finish1<DT>(p, q0 + c + j, prow, v[j]);
+    }
+  } else {
+#pragma unroll 1
+    for (int c = c0; c < c0 + kShare; c += 16) {
+      float v[16];
+      add_parts<S, 4, 4>(part, c, row, v);
+      uint32_t acc[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[j] = __float_as_uint(v[j]);
+      finish16<DT>(p, prow, q0 + c, acc, stage);
+    }
+  }
+}
+
+template <int DT, int BN, bool kSwap>
+__global__ void __launch_bounds__(kSplitThreads, 2) mx4_split_kernel(const __grid_constant__ MatmulKernelParams p,
+                                                                    int split) {
+  using L = Split<BN>;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages], done;
+  __shared__ __align__(8) uint64_t full[L::kStages], empty[L::kStages], done;
   __shared__ uint32_t tmem_slot;
   __shared__ int failed;
   unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    for (int s = 0; s < L::kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
     mbar_init(&done, 1);
     failed = 0;
     fence_mbar_init();
   }
-  if (warp == 5) tmem_alloc<1>(&tmem_slot, kTmemColumns);
+  if (warp == 5) tmem_alloc<1>(&tmem_slot, L::kColumns);
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
-  const uint32_t tmem = tmem_slot;
-  const int tm = blockIdx.x % p.tiles_m, tn = blockIdx.x / p.tiles_m;
+  const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
+  const int rank = blockIdx.x % split, tile = blockIdx.x / split;
+  const int tp = tile % p.tiles_p, tq = tile / p.tiles_p;
+  const int k0 = (int)((long long)p.steps * rank / split), n_steps = (int)((long long)p.steps * (rank + 1) / split) - k0;
   grid_dependency_wait();
 
-  if (warp == 4 && lane == 0) {
+  if (warp == 4) {
     const uint64_t pol = l2_evict_normal_policy();
+    const bool one = elect_one();
     int k = 0;
-    for (; k < p.steps; ++k) {
-      const int s = k % kStages;
-      if (!mbar_wait_bounded(&empty[s], ((k / kStages) & 1) ^ 1, kWaitLimitNs)) break;
-      unsigned char *st = smem + s * kStageBytes;
-      mbar_arrive_expect_tx(&full[s], kStageBytes);
-      tensor_load(st, &p.map_a, k * kRowBytes, tm * kBM, &full[s], pol);
-      tensor_load(st + kStageA, &p.map_b, k * kRowBytes, tn * kBN, &full[s], pol);
-      bulk_load(st + kStageA + kStageB, p.scales_a + ((long long)tm * p.steps + k) * kMx4TileBytes, kMx4TileBytes, &full[s], pol);
-      bulk_load(st + kStageA + kStageB + kMx4TileBytes, p.scales_b + ((long long)tn * p.steps + k) * kMx4TileBytes,
-                kMx4TileBytes, &full[s], pol);
-    }
-    if (k < p.steps) {  // gave up: wait for the copies still in flight
-      atomicOr(p.status, kStatusWaitTimeout);
-      atomicExch(&failed, 1);
-      for (int q = k > kStages ? k - kStages : 0; q < k; ++q)
-        mbar_wait_bounded(&full[q % kStages], (q / kStages) & 1, kWaitLimitNs);
-    }
-  } else if (warp == 5 && lane == 0) {
-    int k = 0;
-    for (; k < p.steps; ++k) {
-      const int s = k % kStages;
-      if (!mbar_wait_bounded(&full[s], (k / kStages) & 1, kWaitLimitNs)) break;
-      tcgen05_fence_after();
-      const uint32_t a = smem_addr(smem + s * kStageBytes), b = a + kStageA, sc = b + kStageB;
-      // the scales of a step: A's eight columns, then B's; steps alternate
-      const uint32_t sa = tmem + kTmemScales + (k & 1) * 16, sb = sa + 8;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        scale_copy<1>(sa + 4 * j, scale_desc(sc + j * kMx4AtomBytes));
-        scale_copy<1>(sb + 4 * j, scale_desc(sc + kMx4TileBytes + j * kMx4AtomBytes));
+    for (; k < n_steps; ++k) {
+      const int s = k % L::kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((k / L::kStages) & 1) ^ 1, kWaitLimitNs))) break;
+      unsigned char *st = smem + s * L::kStageBytes, *sc = st + kHalfBytes + BN * kRowBytes;
+      if (one) {
+        mbar_arrive_expect_tx(&full[s], L::kStageBytes);
+        tensor_load(st, &p.map_p, (k0 + k) * kRowBytes, tp * 128, &full[s], pol);
+        tensor_load(st + kHalfBytes, &p.map_q, (k0 + k) * kRowBytes, tq * BN, &full[s], pol);
+        bulk_load(sc, p.scales_p + ((long long)tp * p.steps + k0 + k) * kMx4TileBytes, kMx4TileBytes, &full[s], pol);
+        bulk_load(sc + kMx4TileBytes, p.scales_q + ((long long)tq * p.steps + k0 + k) * kMx4TileBytes, kMx4TileBytes,
+                  &full[s], pol);
       }
+      __syncwarp();
+    }
+    if (k < n_steps) {  // gave up: wait for the copies still in flight
+      if (one) {
+        atomicOr(p.status, kStatusWaitTimeout);
+        atomicExch(&failed, 1);
+      }
+      for (int q = k > L::kStages ? k - L::kStages : 0; q < k; ++q)
+        mbar_wait_bounded(&full[q % L::kStages], (q / L::kStages) & 1, kWaitLimitNs);
+    }
+  } else if (warp == 5) {
+    const bool one = elect_one();
+    int k = 0;
+    for (; k < n_steps; ++k) {
+      const int s = k % L::kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (k / L::kStages) & 1, kWaitLimitNs))) break;
+      tcgen05_fence_after();
+      const uint32_t a = smem_addr(smem) + s * L::kStageBytes, b = a + kHalfBytes, sc = b + BN * kRowBytes;
+      // the scales of a step: P's eight columns, then Q's; a place for each stage
+      const uint32_t sa = tmem + L::kScales + s * 16, sb = sa + 8;
+      if (one) {
 #pragma unroll
-      for (int j = 0; j < kBK / 64; ++j)
-        mx4_mma<1>(tmem, operand_desc(a + 32 * j), operand_desc(b + 32 * j), mx4_instr_desc(kBM, kBN, (j & 1) * 2),
-                sa + 4 * (j / 2), sb + 4 * (j / 2), k > 0 || j > 0);
-      tcgen05_commit<1>(&empty[s]);
+        for (int j = 0; j < 2; ++j) {
+          scale_copy<1>(sa + 4 * j, scale_desc(sc + j * kMx4AtomBytes));
+          scale_copy<1>(sb + 4 * j, scale_desc(sc + kMx4TileBytes + j * kMx4AtomBytes));
+        }
+#pragma unroll
+        for (int j = 0; j < kBK / 64; ++j)
+          mx4_mma<1>(tmem, operand_desc(a + 32 * j), operand_desc(b + 32 * j), mx4_instr_desc(128, BN, (j & 1) * 2),
+                     sa + 4 * (j / 2), sb + 4 * (j / 2), k > 0 || j > 0);
+        tcgen05_commit<1>(&empty[s]);
+      }
+      __syncwarp();
     }
-    if (k < p.steps) {
-      atomicOr(p.status, kStatusWaitTimeout);
-      atomicExch(&failed, 1);
+    if (one) {
+      if (k < n_steps) {
+        atomicOr(p.status, kStatusWaitTimeout);
+        atomicExch(&failed, 1);
+      }
+      tcgen05_commit<1>(&done);
     }
-    tcgen05_commit<1>(&done);
   }
   __syncwarp();
   // every warp waits here for the last product, so none leaves tensor memory
   // or shared memory while they are in use
-  if (!mbar_wait_bounded(&done, 0, 2 * kWaitLimitNs)) {
-    if (lane == 0) {
-      atomicOr(p.status, kStatusWaitTimeout);
-      atomicExch(&failed, 1);
-    }
+  if (!mbar_wait_bounded(&done, 0, 2 * kWaitLimitNs) && lane == 0) {
+    atomicOr(p.status, kStatusWaitTimeout);
+    atomicExch(&failed, 1);
   }
+  __syncwarp();
   tcgen05_fence_after();
   __syncthreads();
 
-  if (warp < 4 && !failed) {
-    const long long row = (long long)tm * kBM + warp * 32 + lane;
+  const int row = warp * 32 + lane;  // of the tile (warps 0-3)
+  const long long prow = (long long)tp * 128 + row;
+  float *part = reinterpret_cast<float *>(smem);  // [BN / 4][128][4]
+  float *stage = part + BN * 128 + warp * kStageFloats;
+  if (warp < 4) {
 #pragma unroll 1
-    for (int c = 0; c < kBN; c += 32) {
-      uint32_t acc[32];
-      tmem_load32(tmem + ((uint32_t)(warp * 32) << 16) + c, acc);
+    for (int c = 0; c < BN; c += 16) {
+      uint32_t acc[16];
+      tmem_load16(tmem + ((uint32_t)(warp * 32) << 16) + c, acc);
       tmem_load_wait();
-if (p.steps == 0) {
+      if (n_steps == 0) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) acc[j] = 0;
+        for (int j = 0; j < 16; ++j) acc[j] = 0;
       }
-      finish16<DT>(p, row, (long long)tn * kBN + c, acc);
-      finish16<DT>(p, row, (long long)tn * kBN + c + 16, acc + 16);
+      if (split > 1) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<uint4 *>(part + ((c + j) / 4 * 128 + row) * 4) = make_uint4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+      } else if (!failed) {
+        if constexpr (kSwap) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) finish1<DT>(p, (long long)tq * BN + c + j, prow, __uint_as_float(acc[j]));
+        } else {
+          finish16<DT>(p, prow, (long long)tq * BN + c, acc, stage);
+        }
+      }
+    }
+  }
+  if (split > 1) {
+    cluster_sync_all();
+    if (warp < 4 && !failed) {
+      const long long q0 = (long long)tq * BN;
+      if (split == 2) finish_split<DT, BN, kSwap, 2>(p, part, rank, row, prow, q0, stage);
+      else if (split == 4) finish_split<DT, BN, kSwap, 4>(p, part, rank, row, prow, q0, stage);
+      else finish_split<DT, BN, kSwap, 8>(p, part, rank, row, prow, q0, stage);
     }
   }
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
-  if (warp == 5) tmem_free<1>(tmem, kTmemColumns);
+  if (warp == 5) tmem_free<1>(tmem, L::kColumns);
+  if (split > 1) cluster_sync_all();  // no CTA leaves while another reads its part
 }
 
 // --------------------------------------------------------------------------
@@ -184,11 +392,12 @@ if (p.steps == 0) {
 // once (128 accumulators a thread) and store it while the next tile's products
 // run.
 constexpr int kPM = 256, kPN = 256;
-constexpr int kPairStages = 6;
-constexpr int kPairHalf = 128 * kRowBytes;  // 128 rows of A or of B
-constexpr int kPairStageBytes = 2 * kPairHalf + 3 * kMx4TileBytes;  // + scales of 128 rows of A, 256 of B
-constexpr int kPairSmemBytes = kPairStages * kPairStageBytes + 1024;
-constexpr int kPairThreads = 320;  // warps 0-7 epilogue, 8 copies, 9 products
+constexpr int kPairStages = 5;
+constexpr int kPairStageBytes = 2 * kHalfBytes + 3 * kMx4TileBytes;  // + scales of 128 rows of A, 256 of B
+constexpr int kPairSmemBytes = kPairStages * kPairStageBytes + 8 * kStageFloats * 4 + 1024;
+constexpr int kPairThreads = 384;  // warps 0-7 epilogue, 8 copies, 9 products, 10 and 11 idle
+// registers a thread: 168 at launch (384 threads), 216 for the two warpgroups
+// of the epilogue and 72 for the third: 2 * 216 + 72 = 3 * 168
 constexpr uint32_t kPairScales = kPN;  // first tensor-memory column of the scales
 
 template <int DT>
@@ -198,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __shared__ __align__(8) uint64_t full[kPairStages], empty[kPairStages], acc_full, acc_empty;
   __shared__ uint32_t tmem_slot;
   unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
   const uint32_t rank = cluster_rank();
 
   if (threadIdx.x == 0) {
@@ -212,75 +421,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync_all();
   tcgen05_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
   const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
-  const long long tiles = (long long)p.tiles_m * p.tiles_n;
+  const long long tiles = (long long)p.tiles_p * p.tiles_q;
   grid_dependency_wait();
 
-  if (warp == 8 && lane == 0) {
-    const uint64_t pol = l2_evict_normal_policy();
-    const int row_tiles_b = (int)ceil_div(p.n, (long long)kMx4TileRows);
-    unsigned g = 0;
-    bool ok = true;
-    for (long long t = pair; t < tiles && ok; t += pairs) {
-      const int tm = (int)(t % p.tiles_m), tn = (int)(t / p.tiles_m);
-      // a scale tile past the end reads as zeros
-      const int ra = tm * 2 + (int)rank, rb = tn * 2, rb1 = rb + 1 < row_tiles_b ? rb + 1 : rb;
-      for (int k = 0; k < p.steps; ++k, ++g) {
-        const unsigned s = g % kPairStages;
-        if (!(ok = mbar_wait_bounded(&empty[s], ((g / kPairStages) & 1) ^ 1, kWaitLimitNs))) break;
-        unsigned char *st = smem + s * kPairStageBytes;
-        const uint32_t bar = cluster_addr(&full[s], 0);
-        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
-        tensor_load_pair(st, &p.map_a, k * kRowBytes, tm * kPM + (int)rank * 128, bar, pol);
-        tensor_load_pair(st + kPairHalf, &p.map_b, k * kRowBytes, tn * kPN + (int)rank * 128, bar, pol);
-        tensor_load_pair(st + 2 * kPairHalf, &p.map_sa, 0, (ra * p.steps + k) * 8, bar, pol);
-        tensor_load_pair(st + 2 * kPairHalf + kMx4TileBytes, &p.map_sb, 0, (rb * p.steps + k) * 8, bar, pol);
-        tensor_load_pair(st + 2 * kPairHalf + 2 * kMx4TileBytes, &p.map_sb, 0, (rb1 * p.steps + k) * 8, bar, pol);
-      }
-    }
-    if (!ok) {  // gave up: let the copies in flight land (a limit, not a wait on them)
-      atomicOr(p.status, kStatusWaitTimeout);
-      for (int s = 0; s < kPairStages; ++s) mbar_wait_bounded(&full[s], 0, 10000000ull);
-    }
-  } else if (warp == 9 && lane == 0 && rank == 0) {
-    unsigned g = 0, i = 0;
-    bool ok = true;
-    for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
-      if (i > 0 && !(ok = mbar_wait_bounded(&acc_empty, (i - 1) & 1, kWaitLimitNs))) break;
-      tcgen05_fence_after();
-      for (int k = 0; k < p.steps; ++k, ++g) {
-        const unsigned s = g % kPairStages;
-        if (!(ok = mbar_wait_bounded(&full[s], (g / kPairStages) & 1, kWaitLimitNs))) break;
-        tcgen05_fence_after();
-        const uint32_t a = smem_addr(smem + s * kPairStageBytes), b = a + kPairHalf, sc = b + kPairHalf;
-        // the scales of a step: A's eight columns, then B's sixteen; steps alternate
-        const uint32_t sa = tmem + kPairScales + (g & 1) * 32, sb = sa + 8;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          scale_copy<2>(sa + 4 * j, scale_desc(sc + j * kMx4AtomBytes));
-          scale_copy<2>(sb + 8 * j, scale_desc(sc + kMx4TileBytes + j * kMx4AtomBytes));
-          scale_copy<2>(sb + 8 * j + 4, scale_desc(sc + 2 * kMx4TileBytes + j * kMx4AtomBytes));
-        }
-#pragma unroll
-        for (int j = 0; j < kBK / 64; ++j)
-          mx4_mma<2>(tmem, operand_desc(a + 32 * j), operand_desc(b + 32 * j), mx4_instr_desc(kPM, kPN, (j & 1) * 2),
-                     sa + 4 * (j / 2), sb + 8 * (j / 2), k > 0 || j > 0);
-        tcgen05_commit<2>(&empty[s]);
-      }
-      tcgen05_commit<2>(&acc_full);
-    }
-    if (!ok) atomicOr(p.status, kStatusWaitTimeout);
-  } else if (warp < 8) {
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // The residual comes a chunk of columns ahead (the first before the tile is
+    // complete), so its latency hides behind the chunk being finished.
+    constexpr int kChunk = DT == kF32 ? 16 : 32;
     const int quarter = warp % 4, half = warp / 4;
+    float *stage = reinterpret_cast<float *>(smem + kPairStages * kPairStageBytes) + warp * kStageFloats;
     unsigned i = 0;
     for (long long t = pair; t < tiles; t += pairs, ++i) {
-      const int tm = (int)(t % p.tiles_m), tn = (int)(t / p.tiles_m);
-      if (!mbar_wait_bounded(&acc_full, i & 1, kWaitLimitNs)) {
+      const int tp = (int)(t % p.tiles_p), tq = (int)(t / p.tiles_p);
+      const long long rows0 = (long long)tp * kPM + rank * 128 + quarter * 32, row = rows0 + lane;
+      const long long col0 = (long long)tq * kPN + half * 128;
+      const bool aligned = aligned_block<128>(p, col0);
+      uint4 res[2][kChunk / 8 * kRaw8<DT>];
+      if (p.residual && aligned) load_residual<DT, kChunk>(p, row, col0, res[0]);
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&acc_full, i & 1, kWaitLimitNs))) {
         if (lane == 0) atomicOr(p.status, kStatusWaitTimeout);
         break;
       }
-      __syncwarp();
       tcgen05_fence_after();
       uint32_t acc[128];
 #pragma unroll
@@ -290,9 +454,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tcgen05_fence_before();
       __syncwarp();
       if (lane == 0) cluster_arrive_remote(cluster_addr(&acc_empty, 0));
-      const long long row = (long long)tm * kPM + rank * 128 + quarter * 32 + lane;
+      if (aligned) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) finish16<DT>(p, row, (long long)tn * kPN + half * 128 + 16 * c, acc + 16 * c);
+        for (int c = 0; c < 128 / kChunk; ++c) {
+          if (p.residual && c + 1 < 128 / kChunk)
+            load_residual<DT, kChunk>(p, row, col0 + (c + 1) * kChunk, res[(c + 1) & 1]);
+          finish_aligned<DT, kChunk>(p, row, col0 + c * kChunk, acc + c * kChunk, res[c & 1]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) finish_ragged<DT>(p, rows0, col0 + 16 * c, acc + 16 * c, stage);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8) {
+      const uint64_t pol = l2_evict_normal_policy();
+      const bool one = elect_one();
+      const int row_tiles_q = (int)ceil_div(p.n, (long long)kMx4TileRows);
+      unsigned g = 0;
+      bool ok = true;
+      for (long long t = pair; t < tiles && ok; t += pairs) {
+        const int tp = (int)(t % p.tiles_p), tq = (int)(t / p.tiles_p);
+        // (a scale tile of A past the last row reads as zeros)
+        const int ra = tp * 2 + (int)rank, rb = tq * 2, rb1 = rb + 1 < row_tiles_q ? rb + 1 : rb;
+        for (int k = 0; k < p.steps; ++k, ++g) {
+          const unsigned s = g % kPairStages;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((g / kPairStages) & 1) ^ 1, kWaitLimitNs)))) break;
+          unsigned char *st = smem + s * kPairStageBytes;
+          const uint32_t bar = cluster_addr(&full[s], 0);
+          if (one) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
+            tensor_load_pair(st, &p.map_p, k * kRowBytes, tp * kPM + (int)rank * 128, bar, pol);
+            tensor_load_pair(st + kHalfBytes, &p.map_q, k * kRowBytes, tq * kPN + (int)rank * 128, bar, pol);
+            tensor_load_pair(st + 2 * kHalfBytes, &p.map_sp, 0, (ra * p.steps + k) * 8, bar, pol);
+            tensor_load_pair(st + 2 * kHalfBytes + kMx4TileBytes, &p.map_sq, 0, (rb * p.steps + k) * 8, bar, pol);
+            tensor_load_pair(st + 2 * kHalfBytes + 2 * kMx4TileBytes, &p.map_sq, 0, (rb1 * p.steps + k) * 8, bar, pol);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {  // gave up: let the copies in flight land (a limit, not a wait on them)
+        if (one) atomicOr(p.status, kStatusWaitTimeout);
+        for (int s = 0; s < kPairStages; ++s) mbar_wait_bounded(&full[s], 0, 10000000ull);
+      }
+    } else if (warp == 9 && rank == 0) {
+      const bool one = elect_one();
+      unsigned g = 0, i = 0;
+      bool ok = true;
+      for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
+        if (i > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty, (i - 1) & 1, kWaitLimitNs)))) break;
+        tcgen05_fence_after();
+        for (int k = 0; k < p.steps; ++k, ++g) {
+          const unsigned s = g % kPairStages;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (g / kPairStages) & 1, kWaitLimitNs)))) break;
+          tcgen05_fence_after();
+          const uint32_t a = smem_addr(smem) + s * kPairStageBytes, b = a + kHalfBytes, sc = b + kHalfBytes;
+          // the scales of a step: A's eight columns, then B's sixteen; a place for each stage
+          const uint32_t sa = tmem + kPairScales + s * 24, sb = sa + 8;
+          if (one) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              scale_copy<2>(sa + 4 * j, scale_desc(sc + j * kMx4AtomBytes));
+              scale_copy<2>(sb + 8 * j, scale_desc(sc + kMx4TileBytes + j * kMx4AtomBytes));
+              scale_copy<2>(sb + 8 * j + 4, scale_desc(sc + 2 * kMx4TileBytes + j * kMx4AtomBytes));
+            }
+#pragma unroll
+            for (int j = 0; j < kBK / 64; ++j)
+              mx4_mma<2>(tmem, operand_desc(a + 32 * j), operand_desc(b + 32 * j), mx4_instr_desc(kPM, kPN, (j & 1) * 2),
+                         sa + 4 * (j / 2), sb + 8 * (j / 2), k > 0 || j > 0);
+            tcgen05_commit<2>(&empty[s]);
+          }
+          __syncwarp();
+        }
+        if (one) tcgen05_commit<2>(&acc_full);
+      }
+      if (!ok && one) atomicOr(p.status, kStatusWaitTimeout);
     }
   }
   __syncwarp();
@@ -345,8 +582,11 @@ bool make_scale_map(CUtensorMap *map, const uint8_t *scales, long long tiles) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class K>
-cudaError_t launch_matmul(K *k, long long grid, int threads, int smem, const MatmulKernelParams &q, cudaStream_t s) {
+// cluster: CTAs a cluster (given as a launch attribute where the kernel has no
+// size of its own).
+template <class... Args>
+cudaError_t launch_matmul(void (*k)(Args...), long long grid, int threads, int smem, int cluster, cudaStream_t s,
+                          Args... args) {
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -355,36 +595,61 @@ cudaError_t launch_matmul(K *k, long long grid, int threads, int smem, const Mat
   c.blockDim = dim3((unsigned)threads);
   c.dynamicSmemBytes = smem;
   c.stream = s;
-  cudaLaunchAttribute a = {};
-  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &a;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, k, q);
+  cudaLaunchAttribute a[2] = {};
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = (unsigned)cluster, a[1].val.clusterDim.y = 1, a[1].val.clusterDim.z = 1;
+  c.attrs = a;
+  c.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&c, k, args...);
+}
+
+// CTAs a tile.  Up to 64 columns: as many as fit the GPU at two an SM, each with
+// a step or more (1 x 4096 x 4096: 10.1 us whole, 7.8, 6.2 and 5.9 us at 2, 4
+// and 8; 1 x 11008 x 4096, 86 tiles: 10.8, 9.7 and, past two an SM, 12.9 and
+// 16.2 us).  At 128 columns a part is 64 KB to exchange, so at most one CTA an
+// SM and four steps or more each (128 x 4096 x 4096: 11.6, 9.8, 8.8 and 12.8
+// us; 1024^3, 64 tiles of four steps: 6.4 us whole, 7.2 in two).
+int split_of(long long tiles, int steps, int columns, int sms) {
+  const long long most = columns <= 64 ? 2ll * sms : sms;
+  const int least = columns <= 64 ? 1 : 4;
+  int s = 1;
+  while (s < 8 && tiles * s * 2 <= most && s * 2 * least <= steps) s *= 2;
+  return s;
+}
+
+template <int DT, int BN, bool kSwap>
+cudaError_t split_bn(MatmulKernelParams &q, const Mx4Operand &op, const Mx4Operand &oq, int sms, cudaStream_t s) {
+  q.tiles_p = (int)ceil_div(op.rows, 128ll), q.tiles_q = (int)ceil_div(oq.rows, (long long)BN);
+  if (q.steps > 0 && (!make_map(&q.map_p, op, 128) || !make_map(&q.map_q, oq, BN))) return cudaErrorInvalidValue;
+  q.scales_p = op.scales, q.scales_q = oq.scales;
+  const long long tiles = (long long)q.tiles_p * q.tiles_q;
+  const int split = split_of(tiles, q.steps, BN, sms);
+  return launch_matmul(mx4_split_kernel<DT, BN, kSwap>, tiles * split, kSplitThreads, Split<BN>::kSmemBytes, split, s, q,
+                       split);
 }
 
 template <int DT>
 cudaError_t matmul_dt(const MatmulParams &p, cudaStream_t s) {
   MatmulKernelParams q;
-  q.scales_a = p.a.scales, q.scales_b = p.b.scales;
   q.m = p.m, q.n = p.n;
   q.steps = (int)((p.k + kBK - 1) / kBK);
   q.out = p.out, q.residual = p.residual, q.ld_out = p.ld_out, q.ld_res = p.ld_res;
   q.drop = p.drop, q.status = p.status;
   q.vec = p.vec, q.vec32 = p.vec32;
-  const long long ra = ceil_div(p.m, (long long)kMx4TileRows), rb = ceil_div(p.n, (long long)kMx4TileRows);
-  if (p.k > 0 && (!make_map(&q.map_a, p.a, kBM) || !make_map(&q.map_b, p.b, kBN) ||
-                  !make_scale_map(&q.map_sa, p.a.scales, ra * q.steps) ||
-                  !make_scale_map(&q.map_sb, p.b.scales, rb * q.steps)))
-    return cudaErrorInvalidValue;
+  if (p.m <= 16) return split_bn<DT, 16, true>(q, p.b, p.a, p.sms, s);
+  if (p.m <= 32) return split_bn<DT, 32, true>(q, p.b, p.a, p.sms, s);
+  if (p.m <= 64) return split_bn<DT, 64, true>(q, p.b, p.a, p.sms, s);
   const long long pair_tiles = ceil_div(p.m, (long long)kPM) * ceil_div(p.n, (long long)kPN);
-  if (p.k > 0 && pair_tiles >= p.sms / 2) {
-    q.tiles_m = (int)ceil_div(p.m, (long long)kPM), q.tiles_n = (int)ceil_div(p.n, (long long)kPN);
-    const long long grid = 2 * (pair_tiles < p.sms / 2 ? pair_tiles : p.sms / 2);
-    return launch_matmul(mx4_pair_kernel<DT>, grid, kPairThreads, kPairSmemBytes, q, s);
-  }
-  q.tiles_m = (int)ra, q.tiles_n = (int)rb;
-  return launch_matmul(mx4_matmul_kernel<DT>, ra * rb, kMatmulThreads, kSmemBytes, q, s);
+  if (p.k == 0 || pair_tiles < p.sms / 2) return split_bn<DT, 128, false>(q, p.a, p.b, p.sms, s);
+  const long long ra = ceil_div(p.m, (long long)kMx4TileRows), rb = ceil_div(p.n, (long long)kMx4TileRows);
+  if (!make_map(&q.map_p, p.a, 128) || !make_map(&q.map_q, p.b, 128) ||
+      !make_scale_map(&q.map_sp, p.a.scales, ra * q.steps) || !make_scale_map(&q.map_sq, p.b.scales, rb * q.steps))
+    return cudaErrorInvalidValue;
+  q.tiles_p = (int)ceil_div(p.m, (long long)kPM), q.tiles_q = (int)ceil_div(p.n, (long long)kPN);
+  const long long grid = 2 * (pair_tiles < p.sms / 2 ? pair_tiles : p.sms / 2);
+  return launch_matmul(mx4_pair_kernel<DT>, grid, kPairThreads, kPairSmemBytes, 0, s, q);
 }
 
 }  // namespace

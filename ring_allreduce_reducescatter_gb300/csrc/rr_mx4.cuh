@@ -147,6 +147,10 @@ __device__ __forceinline__ void drop8(const DropParams &d, unsigned long long i,
   for (int j = 0; j < 8; ++j) v[j] = number_of(u, j) >= d.threshold ? __fmul_rn(v[j], d.scale) : 0.f;
 }
 
+// Threads of the element-by-element kernels: tx groups of a row by 256 / tx
+// rows a block, rows beyond the grid in a loop.
+constexpr int kFlatThreads = 256;
+
 // --------------------------------------------------------------------------
 // block scales and 4-bit elements
 // --------------------------------------------------------------------------
@@ -187,17 +191,27 @@ __device__ __forceinline__ uint32_t pack8_nearest(const float v[8]) {
 // The same with stochastic rounding.  |v| * 2^-126, rounded toward zero, puts
 // the code in the top bits of a binary32 word: exponent 1 is the code's
 // exponent 1, and the code's subnormal step falls on binary32's subnormals.
-// The 22 bits below are the fraction of a grid step; adding the number to
+// The 22 bits below are the fraction f of a grid step; adding the number to
 // their top 16 carries into the code exactly when floor(f 2^16) + u >= 2^16.
+// Two bits further up the sum leaves the code in the top byte, and byte
+// permutations gather four codes, or four signs, at a time.
 __device__ __forceinline__ uint32_t pack8_stochastic(const float v[8], const uint4 &u) {
-  uint32_t r = 0;
+  const uint32_t n[4] = {u.x, u.y, u.z, u.w};
+  uint32_t s[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const uint32_t w = __float_as_uint(__fmul_rz(fabsf(v[j]), __uint_as_float(0x00800000u)));
-    const uint32_t code = ((w + (number_of(u, j) << 6)) >> 22) | ((__float_as_uint(v[j]) >> 28) & 8u);
-    r |= code << (4 * j);
+    s[j] = w * 4 + __byte_perm(n[j / 2], 0, (j & 1) ? 0x4324 : 0x4104);
   }
-  return r;
+  uint32_t even = __byte_perm(__byte_perm(s[0], s[2], 0x0073), __byte_perm(s[4], s[6], 0x0073), 0x5410);
+  uint32_t odd = __byte_perm(__byte_perm(s[1], s[3], 0x0073), __byte_perm(s[5], s[7], 0x0073), 0x5410);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s[j] = __float_as_uint(v[j]);
+  const uint32_t se = __byte_perm(__byte_perm(s[0], s[2], 0x0073), __byte_perm(s[4], s[6], 0x0073), 0x5410);
+  const uint32_t so = __byte_perm(__byte_perm(s[1], s[3], 0x0073), __byte_perm(s[5], s[7], 0x0073), 0x5410);
+  even |= (se & 0x80808080u) >> 4;
+  odd = odd * 16 | (so & 0x80808080u);
+  return even | odd;
 }
 
 // The values of eight 4-bit codes, times a scale.

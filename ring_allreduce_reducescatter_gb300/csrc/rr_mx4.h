@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ringred.h"
 #include "rr_params.h"
 
@@ -24,6 +26,19 @@ constexpr int kMx4AtomBytes = 512;
 template <class T>
 __host__ __device__ constexpr T ceil_div(T a, T b) {
   return (a + b - 1) / b;
+}
+
+// Allows a kernel its dynamic shared memory, once a device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (done.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_relaxed);
+  return e;
 }
 
 struct Mx4Out {
@@ -46,7 +61,7 @@ struct QuantParams {
   Mx4Out by_rows, by_cols;   // data null: not wanted
   unsigned long long seed, subsequence;  // stochastic rounding (by_cols: subsequence + 1 if both are wanted)
   DropParams drop;
-  int dtype;
+  int dtype, sms;
   bool stochastic;
   bool vec;   // every 16-byte group of a row is aligned
 };
@@ -57,7 +72,7 @@ struct DequantParams {
   void *out;
   long long ld;
   int dtype;
-  bool vec;
+  bool vec, vec32;  // 16- and 32-byte groups of the rows of out are aligned
 };
 
 struct DropoutParams {
@@ -74,7 +89,7 @@ struct Mx4ReduceParams {
   void *out[RR_MAX_RANKS];
   long long rows, cols, row_bytes, tiles_k, base;  // base: floor(rows * cols / R)
   int R, dtype;
-  bool vec;
+  bool vec, vec32;
 };
 
 struct Mx4Operand {
@@ -95,7 +110,14 @@ struct MatmulParams {
   bool vec32;  // every 32-byte group of the rows of out
 };
 
-cudaError_t launch_mx4_quantize(const QuantParams &p, cudaStream_t s);
+cudaError_t launch_mx4_quantize_f32(const QuantParams &p, cudaStream_t s);
+cudaError_t launch_mx4_quantize_f16(const QuantParams &p, cudaStream_t s);
+cudaError_t launch_mx4_quantize_bf16(const QuantParams &p, cudaStream_t s);
+inline cudaError_t launch_mx4_quantize(const QuantParams &p, cudaStream_t s) {
+  return p.dtype == kF32   ? launch_mx4_quantize_f32(p, s)
+         : p.dtype == kF16 ? launch_mx4_quantize_f16(p, s)
+                           : launch_mx4_quantize_bf16(p, s);
+}
 cudaError_t launch_mx4_dequantize(const DequantParams &p, cudaStream_t s);
 cudaError_t launch_dropout(const DropoutParams &p, cudaStream_t s);
 cudaError_t launch_mx4_reduce(const Mx4ReduceParams &p, cudaStream_t s);

@@ -37,6 +37,10 @@ bool aligned16(const void *ptr, size_t rows, size_t ld, size_t E) {
   return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && (rows <= 1 || ld * E % 16 == 0);
 }
 
+bool aligned32(const void *ptr, size_t rows, size_t ld, size_t E) {
+  return reinterpret_cast<uintptr_t>(ptr) % 32 == 0 && (rows <= 1 || ld * E % 32 == 0);
+}
+
 bool extents_ok(size_t rows, size_t cols) {
   return rows <= kMaxExtent && cols <= kMaxExtent && (cols == 0 || rows <= (SIZE_MAX / 64) / cols);
 }
@@ -116,6 +120,9 @@ rr_status ring_mx4_quantize(const void *x, size_t rows, size_t cols, size_t ld, 
   p.dtype = dtype;
   p.stochastic = rounding == RR_MX4_STOCHASTIC;
   p.vec = aligned16(x, rows, ld, E);
+  unsigned *status;
+  const rr_status st = rr::device_info(&status, &p.sms);
+  if (st != RR_OK) return st;
   return launched(rr::launch_mx4_quantize(p, stream));
 }
 
@@ -133,6 +140,7 @@ rr_status ring_mx4_dequantize(const rr_mx4 *q, void *out, size_t ld, rr_dtype dt
   p.rows = o.rows, p.cols = (long long)q->cols, p.row_bytes = o.row_bytes, p.tiles_k = o.tiles_k;
   p.out = out, p.ld = (long long)ld, p.dtype = dtype;
   p.vec = aligned16(out, q->rows, ld, E);
+  p.vec32 = aligned32(out, q->rows, ld, E);
   return launched(rr::launch_mx4_dequantize(p, stream));
 }
 
@@ -159,7 +167,7 @@ rr_status ring_mx4_matmul(const rr_mx4 *a, const rr_mx4 *b, void *out, size_t ld
   p.ld_out = (long long)ld, p.ld_res = (long long)ld_residual;
   p.dtype = dtype;
   p.vec = aligned16(out, m, ld, E) && (!residual || aligned16(residual, m, ld_residual, E));
-  p.vec32 = p.vec && reinterpret_cast<uintptr_t>(out) % 32 == 0 && (m <= 1 || ld * E % 32 == 0);
+  p.vec32 = p.vec && aligned32(out, m, ld, E);
   const rr_status st = rr::device_info(&p.status, &p.sms);
   if (st != RR_OK) return st;
   return launched(rr::launch_mx4_matmul(p, stream));
@@ -200,13 +208,14 @@ rr_status ring_mx4_allreduce(const rr_mx4 *in, void *const *out_bufs, int R, rr_
   rr::Mx4ReduceParams p{};
   Mx4Spans si[RR_MAX_RANKS];
   Span so[RR_MAX_RANKS];
-  p.vec = true;
+  p.vec = p.vec32 = true;
   for (int r = 0; r < R; ++r) {
     if (!mx4_spans(&in[r], &si[r]) || !span_of(out_bufs[r], rows * cols * E, E, &so[r])) return RR_ERR_INVALID_ARG;
     p.data[r] = static_cast<const uint8_t *>(in[r].data);
     p.scales[r] = static_cast<const uint8_t *>(in[r].scales);
     p.out[r] = out_bufs[r];
     p.vec = p.vec && aligned16(out_bufs[r], rows, cols, E);
+    p.vec32 = p.vec32 && aligned32(out_bufs[r], rows, cols, E);
   }
   for (int r = 0; r < R; ++r)
     for (int s = 0; s < R; ++s)

@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mx4_split_kernel(const __gri
   const int tp = tile % p.tiles_p, tq = tile / p.tiles_p;
   const int k0 = (int)((long long)p.steps * rank / split), n_steps = (int)((long long)p.steps * (rank + 1) / split) - k0;
   grid_dependency_wait();
+  grid_dependents_launch();
 
   if (warp == 4) {
     const uint64_t pol = l2_evict_normal_policy();
@@ -425,6 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
   const long long tiles = (long long)p.tiles_p * p.tiles_q;
   grid_dependency_wait();
+  grid_dependents_launch();
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -584,11 +586,10 @@ bool make_scale_map(CUtensorMap *map, const uint8_t *scales, long long tiles) {
 
 // cluster: CTAs a cluster (given as a launch attribute where the kernel has no
 // size of its own).
-template <class... Args>
-cudaError_t launch_matmul(void (*k)(Args...), long long grid, int threads, int smem, int cluster, cudaStream_t s,
-                          Args... args) {
+template <auto kKernel, class... Args>
+cudaError_t launch_matmul(long long grid, int threads, int smem, int cluster, cudaStream_t s, const Args &...args) {
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const cudaError_t e = allow_smem<kKernel>(smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)grid);
@@ -602,7 +603,7 @@ cudaError_t launch_matmul(void (*k)(Args...), long long grid, int threads, int s
   a[1].val.clusterDim.x = (unsigned)cluster, a[1].val.clusterDim.y = 1, a[1].val.clusterDim.z = 1;
   c.attrs = a;
   c.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&c, k, args...);
+  return cudaLaunchKernelEx(&c, kKernel, args...);
 }
 
 // CTAs a tile.  Up to 64 columns: as many as fit the GPU at two an SM, each with
@@ -626,8 +627,8 @@ cudaError_t split_bn(MatmulKernelParams &q, const Mx4Operand &op, const Mx4Opera
   q.scales_p = op.scales, q.scales_q = oq.scales;
   const long long tiles = (long long)q.tiles_p * q.tiles_q;
   const int split = split_of(tiles, q.steps, BN, sms);
-  return launch_matmul(mx4_split_kernel<DT, BN, kSwap>, tiles * split, kSplitThreads, Split<BN>::kSmemBytes, split, s, q,
-                       split);
+  return launch_matmul<mx4_split_kernel<DT, BN, kSwap>>(tiles * split, kSplitThreads, Split<BN>::kSmemBytes, split, s, q,
+                                                        split);
 }
 
 template <int DT>
@@ -649,7 +650,7 @@ cudaError_t matmul_dt(const MatmulParams &p, cudaStream_t s) {
     return cudaErrorInvalidValue;
   q.tiles_p = (int)ceil_div(p.m, (long long)kPM), q.tiles_q = (int)ceil_div(p.n, (long long)kPN);
   const long long grid = 2 * (pair_tiles < p.sms / 2 ? pair_tiles : p.sms / 2);
-  return launch_matmul(mx4_pair_kernel<DT>, grid, kPairThreads, kPairSmemBytes, 0, s, q);
+  return launch_matmul<mx4_pair_kernel<DT>>(grid, kPairThreads, kPairSmemBytes, 0, s, q);
 }
 
 }  // namespace

@@ -1,0 +1,359 @@
+// rr_mx4_quantize.cuh -- quantisation to microscaled 4 bits of one storage
+// format (compiled once for each by rr_mx4_quantize_*.cu).
+//
+// Bound by memory where the rounding is to nearest: the input is read once,
+// 17/32 of a byte an element and direction written.  Stochastic rounding adds
+// a call of the generator for every eight elements and direction, and then the
+// instruction rate bounds it.
+#pragma once
+
+#include "rr_mx4.cuh"
+
+namespace rr {
+
+namespace mx4q {
+
+__device__ __forceinline__ void copy_async16(void *smem_dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem_dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Sixteen bytes of storage elements, of which the first `valid` exist.
+template <int DT>
+__device__ __forceinline__ uint4 load16(const void *base, long long at, int valid, bool vec) {
+  constexpr int E = 16 / Fmt<DT>::bytes;
+  const uint8_t *p = static_cast<const uint8_t *>(base) + at * Fmt<DT>::bytes;
+  if (vec && valid >= E) return ldg_stream(p);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < E; ++j)
+    if (j < valid) {
+      if constexpr (DT == kF32) w[j] = reinterpret_cast<const uint32_t *>(p)[j];
+      else w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[j] << (16 * (j & 1));
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Running maximum of magnitudes: of the two halves of a word apart for 16-bit
+// formats (their bit patterns order like the values), of the word for binary32.
+template <int DT>
+__device__ __forceinline__ uint32_t max_mag(uint32_t m, uint32_t w) {
+  if constexpr (DT == kF32) return max(m, w & 0x7fffffffu);
+  else return __vmaxu2(m, w & 0x7fff7fffu);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t mag_bits(uint32_t m, int half) {  // as binary32 bits
+  if constexpr (DT == kF32) return m;
+  const uint32_t h = half ? m >> 16 : m & 0xffffu;
+  if constexpr (DT == kBF16) return h << 16;
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)h)));
+}
+// The largest magnitude of eight elements, as its own bits.
+template <int DT>
+__device__ __forceinline__ uint32_t max_mag8(const uint4 *raw) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < kRaw8<DT>; ++j)
+    m = max_mag<DT>(max_mag<DT>(max_mag<DT>(max_mag<DT>(m, raw[j].x), raw[j].y), raw[j].z), raw[j].w);
+  return DT == kF32 ? m : max(m & 0xffffu, m >> 16);
+}
+
+// Zeroes the dropped ones of eight elements.
+template <int DT>
+__device__ __forceinline__ void mask8(const DropParams &d, unsigned long long i, uint4 *raw) {
+  const uint4 u = numbers8(d.seed, d.subsequence, d.first + i);
+  uint32_t *w = &raw[0].x;
+  const uint32_t n[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const bool lo = (n[j] & 0xffffu) >= d.threshold, hi = (n[j] >> 16) >= d.threshold;
+    if constexpr (DT == kF32) {
+      if (!lo) w[2 * j] = 0;
+      if (!hi) w[2 * j + 1] = 0;
+    } else {
+      w[j] &= (lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u);
+    }
+  }
+}
+
+// Eight elements of one block to codes.
+template <bool SR, bool DROP>
+__device__ __forceinline__ uint32_t codes8(float v[8], uint32_t byte, float dscale, unsigned long long seed,
+                                           unsigned long long sub, unsigned long long group) {
+  const float inv = inverse_scale(byte);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if constexpr (DROP) v[j] = __fmul_rn(v[j], dscale);
+    v[j] = __fmul_rn(v[j], inv);
+  }
+  uint32_t q;
+  if constexpr (SR) q = pack8_stochastic(v, philox(seed, sub, group));
+  else q = pack8_nearest(v);
+  return byte == 255u ? 0u : q;
+}
+
+// --------------------------------------------------------------------------
+// along the rows
+// --------------------------------------------------------------------------
+
+// One CTA: 128 rows by 256 columns, the extent of one scale tile.  Warp w
+// takes rows w, w + warps, ...; a lane takes eight neighbours of a row (one
+// counter of the generator, one 32-bit word of codes), four lanes a block.
+// The scales gather in shared memory, so the tile is written whole, its
+// padding as zeros.
+template <int DT, bool SR, bool DROP>
+__global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ QuantParams p) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  __shared__ __align__(16) uint8_t tile[kMx4TileBytes];
+  const Mx4Out &o = p.by_rows;
+  const unsigned tk = blockIdx.x % (unsigned)o.tiles_k, tr = blockIdx.x / (unsigned)o.tiles_k;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  const long long c0 = (long long)tk * kMx4TileCols + lane * 8, r0 = (long long)tr * kMx4TileRows + warp;
+  const int valid = (int)max(0ll, min(8ll, p.cols - c0));
+  const bool in_row = c0 < o.row_bytes * 2;
+  constexpr int U = 4;  // rows in flight
+#pragma unroll 1
+  for (int k = 0; k < kMx4TileRows; k += U * warps) {
+    uint4 raw[U][kRaw8<DT>];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long r = r0 + k + u * warps;
+#pragma unroll
+      for (int j = 0; j < kRaw8<DT>; ++j)
+        raw[u][j] = r < p.rows ? load16<DT>(p.x, r * p.ld + c0 + 4 * j, valid - 4 * j, p.vec) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long r = r0 + k + u * warps;
+      const int rl = warp + k + u * warps;
+      uint32_t byte = 0;
+      if (r < p.rows) {  // the same for the whole warp
+        if constexpr (DROP) mask8<DT>(p.drop, (unsigned long long)(r * p.cols + c0), raw[u]);
+        uint32_t m = max_mag8<DT>(raw[u]);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        m = mag_bits<DT>(m, 0);
+        if constexpr (DROP) m = __float_as_uint(__fmul_rn(__uint_as_float(m), p.drop.scale));
+        byte = scale_byte(m);
+        float v[8];
+        widen8<DT>(raw[u], v);
+        const uint32_t q = codes8<SR, DROP>(v, byte, p.drop.scale, p.seed, p.subsequence,
+                                            (unsigned long long)(r * o.row_bytes * 2 + c0) >> 3);
+        if (in_row) *reinterpret_cast<uint32_t *>(o.data + r * o.row_bytes + c0 / 2) = q;
+      }
+      if ((lane & 3) == 0)
+        tile[(lane >> 4) * kMx4AtomBytes + (rl & 31) * 16 + (rl >> 5) * 4 + ((lane >> 2) & 3)] = (uint8_t)byte;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < kMx4TileBytes / 16)
+    reinterpret_cast<uint4 *>(o.scales + ((long long)tr * o.tiles_k + tk) * kMx4TileBytes)[threadIdx.x] =
+        reinterpret_cast<const uint4 *>(tile)[threadIdx.x];
+}
+
+// --------------------------------------------------------------------------
+// along the columns (the result is the transpose), with or without the rows
+// --------------------------------------------------------------------------
+
+// One CTA: 128 rows by W columns (512 bytes a row), brought to shared memory
+// by asynchronous copies, three CTAs an SM, so that one's loads run under
+// another's arithmetic.  First the rows (a lane eight neighbours, four lanes a
+// block; dropout is applied in place here), then the columns: a lane takes the
+// 32-bit word of one column, or two, down 32 rows, a whole block in
+// registers, two blocks one after the other, 32 bytes of codes.  (Holding the
+// tile in registers instead, 32 rows a lane, spilled: 47 us for both ways of
+// 8192 x 4096 bfloat16.)
+constexpr int kTileThreads = 256;
+constexpr int kTileRowBytes = 512;
+constexpr int kTileSmem = kMx4TileRows * kTileRowBytes;
+
+template <int DT, bool SR, bool DROP, bool ROWS>
+__global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_constant__ QuantParams p,
+                                                                  unsigned tiles_c, bool out32) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  constexpr int E = 16 / Fmt<DT>::bytes;              // elements in 16 bytes
+  constexpr int W = kTileRowBytes / Fmt<DT>::bytes;   // columns of the CTA
+  constexpr int C = 4 / Fmt<DT>::bytes;               // columns in 32 bits
+  extern __shared__ __align__(16) unsigned char x[];  // [128][512]
+  __shared__ __align__(16) uint8_t scales_r[W / 128][kMx4AtomBytes];
+  __shared__ __align__(16) uint8_t scales_c[W / 128][kMx4AtomBytes];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const unsigned tc = blockIdx.x % tiles_c, tr = blockIdx.x / tiles_c;
+  const long long row0 = (long long)tr * kMx4TileRows, col0 = (long long)tc * W;
+  const float dscale = DROP ? p.drop.scale : 1.f;
+
+  {
+    const int c = (threadIdx.x % 32) * E;
+    const int valid = (int)max(0ll, min((long long)E, p.cols - col0 - c));
+#pragma unroll
+    for (int k = 0; k < kMx4TileRows / 8; ++k) {
+      const int r = warp + 8 * k;
+      unsigned char *dst = x + r * kTileRowBytes + (threadIdx.x % 32) * 16;
+      const long long at = (row0 + r) * p.ld + col0 + c;
+      if (row0 + r < p.rows && p.vec && valid == E)
+        copy_async16(dst, static_cast<const uint8_t *>(p.x) + at * Fmt<DT>::bytes);
+      else
+        *reinterpret_cast<uint4 *>(dst) =
+            row0 + r < p.rows ? load16<DT>(p.x, at, valid, false) : make_uint4(0, 0, 0, 0);
+    }
+    copy_async_wait();
+  }
+  __syncthreads();
+
+  if constexpr (ROWS || DROP) {
+    constexpr int L = W / 8;  // lanes a row
+    const Mx4Out &o = p.by_rows;
+    const int cl = lane % L * 8;
+    const long long c0 = col0 + cl;
+#pragma unroll 2
+    for (int k = 0; k < 16; k += 32 / L) {
+      const int rl = warp * 16 + k + lane / L;
+      const long long r = row0 + rl;
+      uint4 raw[kRaw8<DT>];
+      uint4 *at = reinterpret_cast<uint4 *>(x + rl * kTileRowBytes + cl * Fmt<DT>::bytes);
+#pragma unroll
+      for (int j = 0; j < kRaw8<DT>; ++j) raw[j] = at[j];
+      if constexpr (DROP) {
+        mask8<DT>(p.drop, (unsigned long long)(r * p.cols + c0), raw);
+#pragma unroll
+        for (int j = 0; j < kRaw8<DT>; ++j) at[j] = raw[j];
+      }
+      if constexpr (ROWS) {
+        uint32_t m = max_mag8<DT>(raw);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        m = mag_bits<DT>(m, 0);
+        if constexpr (DROP) m = __float_as_uint(__fmul_rn(__uint_as_float(m), dscale));
+        const uint32_t byte = scale_byte(m);
+        float v[8];
+        widen8<DT>(raw, v);
+        const long long i = r * o.row_bytes * 2 + c0;
+        const uint32_t q = codes8<SR, DROP>(v, byte, dscale, p.seed, p.subsequence, (unsigned long long)i >> 3);
+        if (r < p.rows && c0 < o.row_bytes * 2) *reinterpret_cast<uint32_t *>(o.data + i / 2) = q;
+        if ((lane & 3) == 0) scales_r[cl >> 7][(rl & 31) * 16 + (rl >> 5) * 4 + ((cl >> 5) & 3)] = (uint8_t)byte;
+      }
+    }
+    if constexpr (DROP) __syncthreads();
+  }
+
+  const Mx4Out &o = p.by_cols;
+  const unsigned long long sub = p.subsequence + (ROWS ? 1 : 0);
+  const int half = warp & 1, cl = (warp >> 1) * 32 * C + lane * C;  // 64 of the rows; the lane's first column
+  uint4 codes[C][2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    const int rl = half * 64 + b * 32;
+    uint32_t w[32];
+    uint32_t m = 0;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      w[r] = *reinterpret_cast<const uint32_t *>(x + (rl + r) * kTileRowBytes + cl * Fmt<DT>::bytes);
+      m = max_mag<DT>(m, w[r]);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      uint32_t mc = mag_bits<DT>(m, c);
+      if constexpr (DROP) mc = __float_as_uint(__fmul_rn(__uint_as_float(mc), dscale));
+      const uint32_t byte = scale_byte(mc);
+      uint32_t q[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t y = w[8 * g + e];
+          if constexpr (DT == kF32) v[e] = __uint_as_float(y);
+          else if constexpr (DT == kBF16) v[e] = __uint_as_float(c ? y & 0xffff0000u : y << 16);
+          else v[e] = c ? __high2float(as_h2(y)) : __low2float(as_h2(y));
+        }
+        q[g] = codes8<SR, DROP>(v, byte, dscale, p.seed, sub,
+                                (unsigned long long)((col0 + cl + c) * o.row_bytes * 2 + row0 + rl + 8 * g) >> 3);
+      }
+      codes[c][b] = make_uint4(q[0], q[1], q[2], q[3]);
+      const int cc = cl + c;
+      scales_c[cc >> 7][(cc & 31) * 16 + ((cc >> 5) & 3) * 4 + half * 2 + b] = (uint8_t)byte;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const long long col = col0 + cl + c, row = row0 + half * 64;
+    if (col >= p.cols || row >= p.rows) continue;
+    uint8_t *q = o.data + col * o.row_bytes + row / 2;
+    if (out32 && row + 32 < p.rows) {
+      stg32(q, codes[c][0], codes[c][1]);
+    } else {
+      *reinterpret_cast<uint4 *>(q) = codes[c][0];
+      if (row + 32 < p.rows) *reinterpret_cast<uint4 *>(q + 16) = codes[c][1];
+    }
+  }
+  __syncthreads();
+  // the scales: an atom is 128 columns by this CTA's four blocks
+  for (int k = threadIdx.x; k < W / 128 * (kMx4AtomBytes / 16); k += kTileThreads) {
+    const int a = k / (kMx4AtomBytes / 16), w = k % (kMx4AtomBytes / 16);
+    const long long rb = (long long)tc * (W / 128) + a;  // 128 rows of the result
+    if (rb * kMx4TileRows < p.cols)
+      reinterpret_cast<uint4 *>(o.scales + (rb * o.tiles_k + tr / 2) * kMx4TileBytes + (tr & 1) * kMx4AtomBytes)[w] =
+          reinterpret_cast<const uint4 *>(scales_c[a])[w];
+    if constexpr (ROWS) {
+      const Mx4Out &q = p.by_rows;
+      const long long atom = (long long)tc * (W / 128) + a;  // 128 columns
+      if (row0 < p.rows && atom / 2 < q.tiles_k)
+        reinterpret_cast<uint4 *>(q.scales + (tr * q.tiles_k + atom / 2) * kMx4TileBytes + (atom & 1) * kMx4AtomBytes)[w] =
+            reinterpret_cast<const uint4 *>(scales_r[a])[w];
+    }
+  }
+}
+
+template <auto kKernel, class... Args>
+cudaError_t launch(long long grid, int threads, int smem, cudaStream_t s, const Args &...args) {
+  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  if (smem > 0) {
+    const cudaError_t e = allow_smem<kKernel>(smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = s;
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kKernel, args...);
+}
+
+template <int DT, bool SR, bool DROP>
+cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
+  if (!p.by_cols.data) {
+    const long long grid = ceil_div(p.rows, (long long)kMx4TileRows) * p.by_rows.tiles_k;
+    // few tiles: more warps share a tile's rows (64 x 4096 is 16 tiles)
+    const int threads = grid >= 2ll * p.sms ? 128 : 512;
+    return launch<mx4_rows_kernel<DT, SR, DROP>>(grid, threads, 0, s, p);
+  }
+  // an even number of tiles of 128 rows (a scale tile of the result spans 256
+  // rows), and columns to whole scale tiles of both results
+  constexpr int W = kTileRowBytes / Fmt<DT>::bytes;
+  const long long tiles_r = 2 * p.by_cols.tiles_k;
+  const long long tiles_c = ceil_div(p.cols, (long long)kMx4TileCols) * (kMx4TileCols / W);
+  const bool out32 = (reinterpret_cast<uintptr_t>(p.by_cols.data) | (uintptr_t)p.by_cols.row_bytes) % 32 == 0;
+  if (p.by_rows.data)
+    return launch<mx4_tile_kernel<DT, SR, DROP, true>>(tiles_r * tiles_c, kTileThreads, kTileSmem, s, p,
+                                                       (unsigned)tiles_c, out32);
+  return launch<mx4_tile_kernel<DT, SR, DROP, false>>(tiles_r * tiles_c, kTileThreads, kTileSmem, s, p,
+                                                      (unsigned)tiles_c, out32);
+}
+
+template <int DT>
+cudaError_t quantize_any(const QuantParams &p, cudaStream_t s) {
+  const bool drop = p.drop.threshold != 0;
+  if (p.stochastic) return drop ? quantize_dt<DT, true, true>(p, s) : quantize_dt<DT, true, false>(p, s);
+  return drop ? quantize_dt<DT, false, true>(p, s) : quantize_dt<DT, false, false>(p, s);
+}
+
+}  // namespace mx4q
+
+}  // namespace rr

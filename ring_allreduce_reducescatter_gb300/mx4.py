@@ -78,7 +78,7 @@ class Mx4:
     [rows, 16 * ceil(cols / 32)], and ``scales``, uint8
     [ceil(rows / 128), ceil(cols / 256), 1024]."""
 
-    __slots__ = ("data", "scales", "rows", "cols", "_c", "_at")
+    __slots__ = ("rows", "cols", "device", "_data", "_scales", "_whole", "_c", "_at")
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
         if rows < 0 or cols < 0:
@@ -91,74 +91,79 @@ class Mx4:
                 raise ValueError(f"{name}: {t.numel()} bytes, expected {n} for {rows} x {cols}")
         if scales.device != data.device:
             raise ValueError("data and scales must be on one device")
-        self._set(data, scales, rows, cols)
-
-    def _set(self, data, scales, rows, cols):
-        self.data, self.scales, self.rows, self.cols = data, scales, rows, cols
+        self.rows, self.cols, self.device = rows, cols, data.device
+        self._data, self._scales, self._whole = data, scales, None
         self._c = _Matrix(data.data_ptr(), scales.data_ptr(), rows, cols)
         self._at = ctypes.addressof(self._c)
-        return self
 
     @classmethod
     def empty(cls, rows: int, cols: int, device=None) -> "Mx4":
-        """A matrix whose bytes are not set yet."""
+        """A matrix whose bytes are not set yet, in one allocation."""
         if rows < 0 or cols < 0:
             raise ValueError("rows and cols must not be negative")
-        device = torch.device("cuda") if device is None else device
-        return cls.__new__(cls)._set(
-            torch.empty((rows, -(-cols // 32) * 16), dtype=torch.uint8, device=device),
-            torch.empty((-(-rows // 128), -(-cols // 256), 1024), dtype=torch.uint8, device=device), rows, cols)
+        self = cls.__new__(cls)
+        n = rows * (-(-cols // 32) * 16)
+        whole = torch.empty(n + -(-rows // 128) * (-(-cols // 256) * 1024), dtype=torch.uint8,
+                            device="cuda" if device is None else device)
+        at = whole.data_ptr()
+        self.rows, self.cols, self.device = rows, cols, whole.device
+        self._data, self._scales, self._whole = None, n, whole
+        self._c = _Matrix(at, at + n, rows, cols)
+        self._at = ctypes.addressof(self._c)
+        return self
+
+    @property
+    def data(self) -> torch.Tensor:
+        if self._whole is not None:
+            self._split()
+        return self._data
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._whole is not None:
+            self._split()
+        return self._scales
+
+    def _split(self):
+        n, whole = self._scales, self._whole
+        self._data = whole[:n].view(self.rows, -(-self.cols // 32) * 16)
+        self._scales = whole[n:].view(-(-self.rows // 128), -(-self.cols // 256), 1024)
+        self._whole = None
 
     @property
     def shape(self) -> Tuple[int, int]:
         return self.rows, self.cols
 
-    @property
-    def device(self):
-        return self.data.device
-
-    def _tensors(self):
-        return self.data, self.scales
-
     def __repr__(self):
-        return f"Mx4({self.rows} x {self.cols}, {self.data.device})"
+        return f"Mx4({self.rows} x {self.cols}, {self.device})"
 
 
-class _On:
-    """The stream of one call: its handle, allocation on it, and the record
-    that keeps the call's tensors alive on it when it is not the current one."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    __slots__ = ("handle", "_stream", "_outer")
 
-    def __init__(self, device, stream):
-        if device.index is not None and device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-        self._outer = self._stream = None
-        if stream is None:
-            self.handle = torch.cuda.current_stream().cuda_stream or None
-            return
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-        self.handle = stream.cuda_stream or None
-        if stream != torch.cuda.current_stream():
-            self._stream = stream
+def _current(device):
+    """The handle of the device's current stream; the device must be the current one."""
+    at = torch.cuda.current_device()
+    if device.index != at:
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{at}")
+    return (_raw_stream(at) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream) or None
 
-    def __enter__(self):
-        if self._stream is not None:
-            self._outer = torch.cuda.stream(self._stream)
-            self._outer.__enter__()
-        return self
 
-    def __exit__(self, *exc):
-        if self._outer is not None:
-            self._outer.__exit__(*exc)
-
-    def used(self, *tensors):
-        if self._stream is not None:
-            for t in tensors:
-                if t is not None:
-                    for u in t._tensors() if isinstance(t, Mx4) else (t,):
-                        u.record_stream(self._stream)
+def _on(stream, call, *args):
+    """call(*args) with `stream` current, so that its outputs are allocated for
+    that stream, and its tensors kept from reuse until the stream is past it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in args + (out if isinstance(out, tuple) else (out,)):
+        for u in t if isinstance(t, (list, tuple)) else (t,):
+            if isinstance(u, Mx4):
+                for part in (u._whole,) if u._whole is not None else (u._data, u._scales):
+                    part.record_stream(stream)
+            elif isinstance(u, torch.Tensor):
+                u.record_stream(stream)
+    return out
 
 
 def _dtype(t: torch.dtype) -> int:
@@ -187,25 +192,24 @@ def _drop(d: Optional[Dropout]):
     return ctypes.byref(_Drop(d.p, d.seed & _U64, d.subsequence & _U64, d.first & _U64))
 
 
-def _quantize(x, want_rows, want_cols, rounding, seed, subsequence, dropout, out_rows, out_cols, stream):
+def _quantize(x, want_rows, want_cols, rounding, seed, subsequence, dropout, out_rows, out_cols):
     rows, cols, ld = _matrix(x, "x")
+    device = x.device
+    handle = _current(device)
     code = _dtype(x.dtype)
-    try:
-        how = _ROUNDING[rounding]
-    except KeyError:
-        raise ValueError(f"rounding {rounding!r}: 'nearest' or 'stochastic' is wanted") from None
-    with _On(x.device, stream) as on:
-        if want_rows and out_rows is None:
-            out_rows = Mx4.empty(rows, cols, x.device)
-        if want_cols and out_cols is None:
-            out_cols = Mx4.empty(cols, rows, x.device)
-        for q in (out_rows, out_cols):
-            if q is not None and q.device != x.device:
-                raise ValueError(f"out is on {q.device}, x on {x.device}")
-        _check(_lib().ring_mx4_quantize(x.data_ptr(), rows, cols, ld, code, out_rows and out_rows._at,
-                                        out_cols and out_cols._at, how, seed & _U64, subsequence & _U64,
-                                        _drop(dropout), on.handle), "ring_mx4_quantize")
-        on.used(x, out_rows, out_cols)
+    how = _ROUNDING.get(rounding)
+    if how is None:
+        raise ValueError(f"rounding {rounding!r}: 'nearest' or 'stochastic' is wanted")
+    if want_rows and out_rows is None:
+        out_rows = Mx4.empty(rows, cols, device)
+    if want_cols and out_cols is None:
+        out_cols = Mx4.empty(cols, rows, device)
+    for q in (out_rows, out_cols):
+        if q is not None and q.device != device:
+            raise ValueError(f"out is on {q.device}, x on {device}")
+    _check(_lib().ring_mx4_quantize(x.data_ptr(), rows, cols, ld, code, None if out_rows is None else out_rows._at,
+                                    None if out_cols is None else out_cols._at, how, seed & _U64,
+                                    subsequence & _U64, _drop(dropout), handle), "ring_mx4_quantize")
     return out_rows, out_cols
 
 
@@ -214,31 +218,35 @@ def mx4_quantize(x: torch.Tensor, transposed: bool = False, rounding: str = "nea
                  stream=None) -> Mx4:
     """x (two dimensions) in 4 bits along its rows; transposed: the transpose
     of x, along its own rows (x's columns).  dropout is applied to x first."""
+    if stream is not None:
+        return _on(stream, mx4_quantize, x, transposed, rounding, seed, subsequence, dropout, out)
     if transposed:
-        return _quantize(x, False, True, rounding, seed, subsequence, dropout, None, out, stream)[1]
-    return _quantize(x, True, False, rounding, seed, subsequence, dropout, out, None, stream)[0]
+        return _quantize(x, False, True, rounding, seed, subsequence, dropout, None, out)[1]
+    return _quantize(x, True, False, rounding, seed, subsequence, dropout, out, None)[0]
 
 
 def mx4_quantize_both(x: torch.Tensor, rounding: str = "nearest", seed: int = 0, subsequence: int = 0,
                       dropout: Optional[Dropout] = None, stream=None) -> Tuple[Mx4, Mx4]:
     """x and its transpose in 4 bits, x read once (stochastic rounding of the
     transpose takes subsequence + 1)."""
-    return _quantize(x, True, True, rounding, seed, subsequence, dropout, None, None, stream)
+    if stream is not None:
+        return _on(stream, mx4_quantize_both, x, rounding, seed, subsequence, dropout)
+    return _quantize(x, True, True, rounding, seed, subsequence, dropout, None, None)
 
 
 def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
                    stream=None) -> torch.Tensor:
     """The values of a 4-bit matrix, rounded to dtype (exact in binary32 and
     bfloat16, but 4 and 6 times 2^126, which lie above both: infinity)."""
-    with _On(q.device, stream) as on:
-        if out is None:
-            out = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device)
-            ld = q.cols
-        else:
-            ld = _output(out, q.rows, q.cols, q.device)
-        _check(_lib().ring_mx4_dequantize(q._at, out.data_ptr(), ld, _dtype(out.dtype), on.handle),
-               "ring_mx4_dequantize")
-        on.used(q, out)
+    if stream is not None:
+        return _on(stream, mx4_dequantize, q, dtype, out)
+    handle = _current(q.device)
+    if out is None:
+        code = _dtype(dtype)
+        out, ld = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device), q.cols
+    else:
+        code, ld = _dtype(out.dtype), _output(out, q.rows, q.cols, q.device)
+    _check(_lib().ring_mx4_dequantize(q._at, out.data_ptr(), ld, code, handle), "ring_mx4_dequantize")
     return out
 
 
@@ -255,25 +263,26 @@ def mx4_matmul(a: Mx4, b: Mx4, dtype: torch.dtype = torch.bfloat16, residual: Op
                dropout: Optional[Dropout] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """(residual +) dropout(a @ b.T), a.rows x b.rows; residual has the output's
     dtype (that of ``out`` if it is given) and may be ``out`` itself."""
+    if stream is not None:
+        return _on(stream, mx4_matmul, a, b, dtype, residual, dropout, out)
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
     m, n, device = a.rows, b.rows, a.device
     if b.device != device:
         raise ValueError(f"a is on {device}, b on {b.device}")
+    handle = _current(device)
+    if out is None:
+        code = _dtype(dtype)
+        out, ld = torch.empty((m, n), dtype=dtype, device=device), n
+    else:
+        code, ld = _dtype(out.dtype), _output(out, m, n, device)
     ld_res, res = 0, None
-    with _On(device, stream) as on:
-        if out is None:
-            out = torch.empty((m, n), dtype=dtype, device=device)
-            ld = n
-        else:
-            ld = _output(out, m, n, device)
-        if residual is not None:
-            ld_res, res = _output(residual, m, n, device, "residual"), residual.data_ptr()
-            if residual.dtype != out.dtype:
-                raise ValueError(f"residual: {residual.dtype}, the output is {out.dtype}")
-        _check(_lib().ring_mx4_matmul(a._at, b._at, out.data_ptr(), ld, _dtype(out.dtype), res, ld_res,
-                                      _drop(dropout), on.handle), "ring_mx4_matmul")
-        on.used(a, b, residual, out)
+    if residual is not None:
+        ld_res, res = _output(residual, m, n, device, "residual"), residual.data_ptr()
+        if residual.dtype != out.dtype:
+            raise ValueError(f"residual: {residual.dtype}, the output is {out.dtype}")
+    _check(_lib().ring_mx4_matmul(a._at, b._at, out.data_ptr(), ld, code, res, ld_res, _drop(dropout), handle),
+           "ring_mx4_matmul")
     return out
 
 
@@ -282,25 +291,31 @@ def dropout(x: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] = N
     """(residual +) dropout(x).  The backward pass is dropout(dy, drop) with the
     same ``drop``.  Contiguous tensors of any shape, or two-dimensional views
     with neighbouring columns."""
+    if stream is not None:
+        return _on(stream, _dropout, x, drop, residual, out)
+    return _dropout(x, drop, residual, out)
+
+
+def _dropout(x, drop, residual, out):
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x: needs a CUDA tensor")
-    code = _dtype(x.dtype)
-    with _On(x.device, stream) as on:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        ts = (x, out) if residual is None else (x, out, residual)
-        if any(t.shape != x.shape or t.dtype != x.dtype or t.device != x.device for t in ts):
+    code, device, flat = _dtype(x.dtype), x.device, x.is_contiguous()
+    handle = _current(device)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+    for t in (out,) if residual is None else (out, residual):
+        if t.shape != x.shape or t.dtype != x.dtype or t.device != device:
             raise ValueError("x, residual and out must have one shape, dtype and device")
-        if x.is_contiguous() and out.is_contiguous() and (residual is None or residual.is_contiguous()):
-            rows, cols = 1, x.numel()
-            lds = [cols] * 3
-        else:
-            rows, cols = _matrix(x, "x")[:2]
-            lds = [_matrix(t, "x, residual and out")[2] for t in ts] + [cols]
-        _check(_lib().ring_dropout(x.data_ptr(), lds[0], None if residual is None else residual.data_ptr(),
-                                   lds[2], out.data_ptr(), lds[1], rows, cols, code, _drop(drop), on.handle),
-               "ring_dropout")
-        on.used(*ts)
+        flat = flat and t.is_contiguous()
+    if flat:
+        rows, ld_x = 1, x.numel()
+        cols = ld_out = ld_res = ld_x
+    else:
+        rows, cols, ld_x = _matrix(x, "x")
+        ld_out = _matrix(out, "out")[2]
+        ld_res = cols if residual is None else _matrix(residual, "residual")[2]
+    _check(_lib().ring_dropout(x.data_ptr(), ld_x, None if residual is None else residual.data_ptr(), ld_res,
+                               out.data_ptr(), ld_out, rows, cols, code, _drop(drop), handle), "ring_dropout")
     return out
 
 
@@ -308,27 +323,29 @@ def mx4_allreduce(qs: Sequence[Mx4], outs: Optional[Sequence[torch.Tensor]] = No
                   dtype: torch.dtype = torch.float32, stream=None):
     """The flat ring's AllReduce of R equal 4-bit matrices: every output holds
     the binary32 fold of their values, rounded once to its dtype."""
+    if stream is not None:
+        return _on(stream, mx4_allreduce, list(qs), None if outs is None else list(outs), dtype)
     qs = list(qs)
     if not qs:
         raise ValueError("qs: need at least one rank")
     R, shape, device = len(qs), qs[0].shape, qs[0].device
-    if any(q.shape != shape or q.device != device for q in qs):
+    if any(q.rows != shape[0] or q.cols != shape[1] or q.device != device for q in qs):
         raise ValueError("qs: every rank's matrix must have one shape and device")
-    with _On(device, stream) as on:
-        if outs is None:
-            outs = [torch.empty(shape, dtype=dtype, device=device) for _ in qs]
-        else:
-            outs = list(outs)
-            if len(outs) != R:
-                raise ValueError("qs and outs must have one matrix per rank")
-            for t in outs:
-                if (not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype != outs[0].dtype
-                        or t.device != device or not t.is_contiguous()):
-                    raise ValueError("outs: contiguous tensors of the matrices' shape and device and one dtype are wanted")
-        mats = (_Matrix * R)(*[q._c for q in qs])
-        ptrs = (ctypes.c_void_p * R)(*[t.data_ptr() for t in outs])
-        _check(_lib().ring_mx4_allreduce(mats, ptrs, R, _dtype(outs[0].dtype), on.handle), "ring_mx4_allreduce")
-        on.used(*qs, *outs)
+    handle = _current(device)
+    if outs is None:
+        _dtype(dtype)
+        outs = [torch.empty(shape, dtype=dtype, device=device) for _ in qs]
+    else:
+        outs = list(outs)
+        if len(outs) != R:
+            raise ValueError("qs and outs must have one matrix per rank")
+        for t in outs:
+            if (not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype != outs[0].dtype
+                    or t.device != device or not t.is_contiguous()):
+                raise ValueError("outs: contiguous tensors of the matrices' shape and device and one dtype are wanted")
+    mats = (_Matrix * R)(*[q._c for q in qs])
+    ptrs = (ctypes.c_void_p * R)(*[t.data_ptr() for t in outs])
+    _check(_lib().ring_mx4_allreduce(mats, ptrs, R, _dtype(outs[0].dtype), handle), "ring_mx4_allreduce")
     return outs
 
 

@@ -12,39 +12,38 @@ namespace rr {
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy
 // as 1, 2, 3", 2011).  The seed is the key, (i / 8, subsequence) the counter;
 // the 128 bits are the 16-bit numbers of elements i .. i + 7, low half first.
-// 16 bits an element: one call per 8 elements costs about 8 instructions an
-// element, where 32 bits would cost 16 and bound dropout below the memory rate.
+// 16 bits an element: one call per 8 elements costs about 5 instructions an
+// element, where 32 bits would cost 10 and bound dropout below the memory rate.
 // --------------------------------------------------------------------------
 
-__device__ __forceinline__ uint4 philox(unsigned long long seed, unsigned long long sub, unsigned long long group) {
-  uint32_t c0 = (uint32_t)group, c1 = (uint32_t)(group >> 32), c2 = (uint32_t)sub, c3 = (uint32_t)(sub >> 32);
-  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+__device__ __forceinline__ uint4 philox(const Generator &gen, unsigned long long group) {
+  uint32_t c0 = (uint32_t)group, c1 = (uint32_t)(group >> 32), c2 = gen.sub_lo, c3 = gen.sub_hi;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const unsigned long long p0 = (unsigned long long)c0 * 0xD2511F53u, p1 = (unsigned long long)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ gen.keys[2 * r];
     c1 = (uint32_t)p1;
-    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ gen.keys[2 * r + 1];
     c3 = (uint32_t)p0;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(c0, c1, c2, c3);
 }
 
 // The numbers of elements i .. i + 7 for any i (two counters where i is not a
 // multiple of 8).
-__device__ __forceinline__ uint4 numbers8(unsigned long long seed, unsigned long long sub, unsigned long long i) {
+__device__ __forceinline__ uint4 numbers8(const Generator &gen, unsigned long long i) {
   const unsigned long long g = i >> 3;
   const int sh = (int)(i & 7) * 2;
-  uint4 a = philox(seed, sub, g);
+  uint4 a = philox(gen, g);
   if (sh == 0) return a;
-  return funnel16(a, philox(seed, sub, g + 1), sh);
+  return funnel16(a, philox(gen, g + 1), sh);
 }
 
-__device__ __forceinline__ uint32_t number_of(const uint4 &u, int j) {
+// Whether element j of eight is kept: its number, in the high half of a word,
+// against the cut (what lies below the high half cannot change the answer).
+__device__ __forceinline__ bool kept(const uint4 &u, int j, uint32_t cut) {
   const uint32_t w = j < 2 ? u.x : j < 4 ? u.y : j < 6 ? u.z : u.w;
-  return (j & 1) ? w >> 16 : w & 0xffffu;
+  return ((j & 1) ? w : w << 16) >= cut;
 }
 
 // --------------------------------------------------------------------------
@@ -141,10 +140,12 @@ __device__ __forceinline__ void stg32(void *p, uint4 a, uint4 b) {
 }
 
 // v[j] *= scale where element i + j is kept, 0 where it is dropped.
-__device__ __forceinline__ void drop8(const DropParams &d, unsigned long long i, float v[8]) {
-  const uint4 u = numbers8(d.seed, d.subsequence, d.first + i);
+__device__ __forceinline__ void drop8(const DropParams &d, const uint4 &u, float v[8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = number_of(u, j) >= d.threshold ? __fmul_rn(v[j], d.scale) : 0.f;
+  for (int j = 0; j < 8; ++j) v[j] = kept(u, j, d.cut) ? __fmul_rn(v[j], d.scale) : 0.f;
+}
+__device__ __forceinline__ void drop8(const DropParams &d, unsigned long long i, float v[8]) {
+  drop8(d, numbers8(d.gen, d.first + i), v);
 }
 
 // Threads of the element-by-element kernels: tx groups of a row by 256 / tx
@@ -188,25 +189,30 @@ __device__ __forceinline__ uint32_t pack8_nearest(const float v[8]) {
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
-// The same with stochastic rounding.  |v| * 2^-126, rounded toward zero, puts
-// the code in the top bits of a binary32 word: exponent 1 is the code's
-// exponent 1, and the code's subnormal step falls on binary32's subnormals.
-// The 22 bits below are the fraction f of a grid step; adding the number to
-// their top 16 carries into the code exactly when floor(f 2^16) + u >= 2^16.
-// Two bits further up the sum leaves the code in the top byte, and byte
-// permutations gather four codes, or four signs, at a time.
-__device__ __forceinline__ uint32_t pack8_stochastic(const float v[8], const uint4 &u) {
+// The same with stochastic rounding, of x with scale byte `byte` (inv = 2^-X).
+// |x| * 2^(-X - 126), rounded toward zero, puts the code in the top bits of a
+// binary32 word: exponent 1 is the code's exponent 1, and the code's subnormal
+// step falls on binary32's subnormals.  The 22 bits below are the fraction f
+// of a grid step; adding the number to their top 16 carries into the code
+// exactly when floor(f 2^16) + u >= 2^16.  Two bits further up the sum leaves
+// the code in the top byte, and byte permutations gather four codes, or four
+// signs, at a time.
+__device__ __forceinline__ uint32_t pack8_stochastic(float x[8], uint32_t byte, float inv, const uint4 &u) {
   const uint32_t n[4] = {u.x, u.y, u.z, u.w};
+  float k = __fmul_rn(inv, __uint_as_float(0x00800000u));  // 2^(-X - 126), exact up to X = 23
+  if (byte > 150u) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], inv);
+    k = __uint_as_float(0x00800000u);
+  }
   uint32_t s[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t w = __float_as_uint(__fmul_rz(fabsf(v[j]), __uint_as_float(0x00800000u)));
-    s[j] = w * 4 + __byte_perm(n[j / 2], 0, (j & 1) ? 0x4324 : 0x4104);
-  }
+  for (int j = 0; j < 8; ++j)
+    s[j] = __float_as_uint(__fmul_rz(fabsf(x[j]), k)) * 4 + __byte_perm(n[j / 2], 0, (j & 1) ? 0x4324 : 0x4104);
   uint32_t even = __byte_perm(__byte_perm(s[0], s[2], 0x0073), __byte_perm(s[4], s[6], 0x0073), 0x5410);
   uint32_t odd = __byte_perm(__byte_perm(s[1], s[3], 0x0073), __byte_perm(s[5], s[7], 0x0073), 0x5410);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = __float_as_uint(v[j]);
+  for (int j = 0; j < 8; ++j) s[j] = __float_as_uint(x[j]);
   const uint32_t se = __byte_perm(__byte_perm(s[0], s[2], 0x0073), __byte_perm(s[4], s[6], 0x0073), 0x5410);
   const uint32_t so = __byte_perm(__byte_perm(s[1], s[3], 0x0073), __byte_perm(s[5], s[7], 0x0073), 0x5410);
   even |= (se & 0x80808080u) >> 4;

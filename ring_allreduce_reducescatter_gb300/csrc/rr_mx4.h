@@ -49,17 +49,36 @@ struct Mx4Out {
   long long tiles_k;     // ceil(cols / 256)
 };
 
+// The generator of one seed and subsequence: the ten rounds' keys, made on the
+// host so that each is an operand from the parameter block (made in the
+// kernels they cost a fifth of the generator's instructions).
+struct Generator {
+  unsigned int keys[20];
+  unsigned int sub_lo, sub_hi;
+};
+inline Generator make_generator(unsigned long long seed, unsigned long long subsequence) {
+  Generator g;
+  unsigned int k0 = (unsigned int)seed, k1 = (unsigned int)(seed >> 32);
+  for (int r = 0; r < 10; ++r) {
+    g.keys[2 * r] = k0, g.keys[2 * r + 1] = k1;
+    k0 += 0x9E3779B9u, k1 += 0xBB67AE85u;
+  }
+  g.sub_lo = (unsigned int)subsequence, g.sub_hi = (unsigned int)(subsequence >> 32);
+  return g;
+}
+
 struct DropParams {
-  unsigned long long seed, subsequence, first;
-  unsigned int threshold;  // kept if the 16-bit number is at least this; 0: everything is kept
-  float scale;             // 65536 / (65536 - threshold)
+  Generator gen;
+  unsigned long long first;
+  unsigned int cut;  // threshold << 16: kept if the 16-bit number, so shifted, is at least this; 0: everything is kept
+  float scale;       // 65536 / (65536 - threshold)
 };
 
 struct QuantParams {
   const void *x;
   long long rows, cols, ld;
   Mx4Out by_rows, by_cols;   // data null: not wanted
-  unsigned long long seed, subsequence;  // stochastic rounding (by_cols: subsequence + 1 if both are wanted)
+  Generator gen_rows, gen_cols;  // stochastic rounding
   DropParams drop;
   int dtype, sms;
   bool stochastic;

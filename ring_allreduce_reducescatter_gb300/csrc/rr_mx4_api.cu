@@ -75,8 +75,9 @@ bool drop_params(const rr_dropout *d, rr::DropParams *o) {
   if (!(d->p >= 0.0 && d->p < 1.0)) return false;
   const unsigned t = (unsigned)floor(d->p * 65536.0 + 0.5);
   if (t > 65535u) return false;
-  o->seed = d->seed, o->subsequence = d->subsequence, o->first = d->first;
-  o->threshold = t;
+  o->gen = rr::make_generator(d->seed, d->subsequence);
+  o->first = d->first;
+  o->cut = t << 16;
   o->scale = (float)(65536.0 / (65536.0 - (double)t));
   return true;
 }
@@ -116,7 +117,8 @@ rr_status ring_mx4_quantize(const void *x, size_t rows, size_t cols, size_t ld, 
   p.x = x;
   p.rows = (long long)rows, p.cols = (long long)cols, p.ld = (long long)ld;
   p.by_rows = mx4_out(by_rows), p.by_cols = mx4_out(by_cols);
-  p.seed = seed, p.subsequence = subsequence;
+  p.gen_rows = rr::make_generator(seed, subsequence);
+  p.gen_cols = rr::make_generator(seed, subsequence + (by_rows ? 1 : 0));
   p.dtype = dtype;
   p.stochastic = rounding == RR_MX4_STOCHASTIC;
   p.vec = aligned16(x, rows, ld, E);

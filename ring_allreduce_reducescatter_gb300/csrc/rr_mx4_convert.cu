@@ -94,41 +94,56 @@ __global__ void __launch_bounds__(kFlatThreads) mx4_values_kernel(const __grid_c
 // dropout
 // --------------------------------------------------------------------------
 
-// The eight elements of a thread are one counter of the generator.
 template <int DT, bool RES>
-__device__ __forceinline__ void dropout8(const DropoutParams &p, long long r, long long c0, const float *in,
-                                         const float *res, int valid) {
-  float v[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = in[j];
-  if (p.drop.threshold) drop8(p.drop, (unsigned long long)(r * p.cols + c0), v);
+__device__ __forceinline__ void dropout8(const DropoutParams &p, unsigned long long i, float *v, const float *res) {
+  if (p.drop.cut) drop8(p.drop, i, v);
   if constexpr (RES) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(res[j], v[j]);
   }
-  store8<DT>(p.out, r * p.ld_out + c0, valid, p.vec, v);
 }
 
-// One long row: a thread takes U groups, a block's groups apart, all loaded
-// before the first call of the generator.
+// One long row: a thread takes U groups of eight (one counter of the generator
+// each), a block's groups apart, all loaded before the first call of the
+// generator.
 template <int DT, bool RES, int U>
 __global__ void __launch_bounds__(kFlatThreads) dropout_flat_kernel(const __grid_constant__ DropoutParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const long long g0 = (long long)blockIdx.x * (kFlatThreads * U) + threadIdx.x;
+  using T = typename Fmt<DT>::type;
+  const long long block0 = (long long)blockIdx.x * (kFlatThreads * U * 8), c0 = block0 + threadIdx.x * 8;
   float v[U][8], w[U][8];
+  if (p.vec && block0 + kFlatThreads * U * 8 <= p.cols) {  // the same for the whole block
+    const T *x = static_cast<const T *>(p.x) + c0, *res = static_cast<const T *>(p.residual) + c0;
+    uint4 raw[U][kRaw8<DT>], rawr[U][kRaw8<DT>];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const long long c0 = (g0 + u * kFlatThreads) * 8;
-    const int valid = (int)max(0ll, min(8ll, p.cols - c0));
-    load8<DT>(p.x, c0, valid, p.vec, v[u]);
-    if constexpr (RES) load8<DT>(p.residual, c0, valid, p.vec, w[u]);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < kRaw8<DT>; ++j) {
+        raw[u][j] = ldg_stream(reinterpret_cast<const uint4 *>(x + u * kFlatThreads * 8) + j);
+        if constexpr (RES) rawr[u][j] = ldg_stream(reinterpret_cast<const uint4 *>(res + u * kFlatThreads * 8) + j);
+      }
+    T *o = static_cast<T *>(p.out) + c0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      widen8<DT>(raw[u], v[u]);
+      if constexpr (RES) widen8<DT>(rawr[u], w[u]);
+      dropout8<DT, RES>(p, (unsigned long long)(c0 + u * kFlatThreads * 8), v[u], w[u]);
+      narrow8<DT>(v[u], raw[u]);
+#pragma unroll
+      for (int j = 0; j < kRaw8<DT>; ++j) stg_stream(reinterpret_cast<uint4 *>(o + u * kFlatThreads * 8) + j, raw[u][j]);
+    }
+    return;
   }
-#pragma unroll
+#pragma unroll 1
   for (int u = 0; u < U; ++u) {
-    const long long c0 = (g0 + u * kFlatThreads) * 8;
-    const int valid = (int)max(0ll, min(8ll, p.cols - c0));
-    if (valid > 0) dropout8<DT, RES>(p, 0, c0, v[u], w[u], valid);
+    const long long c = c0 + u * kFlatThreads * 8;
+    const int valid = (int)max(0ll, min(8ll, p.cols - c));
+    if (valid == 0) break;
+    load8<DT>(p.x, c, valid, p.vec, v[0]);
+    if constexpr (RES) load8<DT>(p.residual, c, valid, p.vec, w[0]);
+    dropout8<DT, RES>(p, (unsigned long long)c, v[0], w[0]);
+    store8<DT>(p.out, c, valid, p.vec, v[0]);
   }
 }
 
@@ -144,7 +159,8 @@ __global__ void __launch_bounds__(kFlatThreads) dropout_rows_kernel(const __grid
     float v[8], w[8];
     load8<DT>(p.x, r * p.ld_x + c0, valid, p.vec, v);
     if constexpr (RES) load8<DT>(p.residual, r * p.ld_res + c0, valid, p.vec, w);
-    dropout8<DT, RES>(p, r, c0, v, w, valid);
+    dropout8<DT, RES>(p, (unsigned long long)(r * p.cols + c0), v, w);
+    store8<DT>(p.out, r * p.ld_out + c0, valid, p.vec, v);
   }
 }
 

@@ -35,14 +35,11 @@ template <int kN>
 __device__ __forceinline__ void drop_row(const MatmulKernelParams &p, long long row, long long col, float v[kN]) {
   const unsigned long long i = p.drop.first + (unsigned long long)(row * p.n + col), g = i >> 3;
   const int sh = (int)(i & 7) * 2;
-  uint4 u = philox(p.drop.seed, p.drop.subsequence, g);
+  uint4 u = philox(p.drop.gen, g);
 #pragma unroll
   for (int h = 0; h < kN / 8; ++h) {
-    const uint4 next = sh == 0 && h + 1 == kN / 8 ? u : philox(p.drop.seed, p.drop.subsequence, g + h + 1);
-    const uint4 w = sh == 0 ? u : funnel16(u, next, sh);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[8 * h + j] = number_of(w, j) >= p.drop.threshold ? __fmul_rn(v[8 * h + j], p.drop.scale) : 0.f;
+    const uint4 next = sh == 0 && h + 1 == kN / 8 ? u : philox(p.drop.gen, g + h + 1);
+    drop8(p.drop, sh == 0 ? u : funnel16(u, next, sh), v + 8 * h);
     u = next;
   }
 }
@@ -74,7 +71,7 @@ __device__ __forceinline__ void finish_aligned(const MatmulKernelParams &p, long
   float v[kN];
 #pragma unroll
   for (int j = 0; j < kN; ++j) v[j] = __uint_as_float(acc[j]);
-  if (p.drop.threshold) drop_row<kN>(p, row, col, v);
+  if (p.drop.cut) drop_row<kN>(p, row, col, v);
   if (p.residual) {
 #pragma unroll
     for (int h = 0; h < kN / 8; ++h) {
@@ -111,7 +108,7 @@ __device__ __forceinline__ void finish_ragged(const MatmulKernelParams &p, long 
   float v[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(acc[j]);
-  if (p.drop.threshold) drop_row<16>(p, rows0 + lane, col, v);
+  if (p.drop.cut) drop_row<16>(p, rows0 + lane, col, v);
 #pragma unroll
   for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = v[j];
   __syncwarp();
@@ -151,10 +148,10 @@ template <int DT>
 __device__ __forceinline__ void finish1(const MatmulKernelParams &p, long long row, long long col, float v) {
   using T = typename Fmt<DT>::type;
   if (row >= p.m || col >= p.n) return;
-  if (p.drop.threshold) {
+  if (p.drop.cut) {
     const unsigned long long i = p.drop.first + (unsigned long long)(row * p.n + col);
-    const uint4 u = philox(p.drop.seed, p.drop.subsequence, i >> 3);
-    v = number_of(u, (int)(i & 7)) >= p.drop.threshold ? __fmul_rn(v, p.drop.scale) : 0.f;
+    const uint4 u = philox(p.drop.gen, i >> 3);
+    v = kept(u, (int)(i & 7), p.drop.cut) ? __fmul_rn(v, p.drop.scale) : 0.f;
   }
   if (p.residual) v = __fadd_rn(to_f32<DT>(static_cast<const T *>(p.residual)[row * p.ld_res + col]), v);
   static_cast<T *>(p.out)[row * p.ld_out + col] = from_f32<DT>(v);

@@ -61,12 +61,11 @@ __device__ __forceinline__ uint32_t max_mag8(const uint4 *raw) {
 // Zeroes the dropped ones of eight elements.
 template <int DT>
 __device__ __forceinline__ void mask8(const DropParams &d, unsigned long long i, uint4 *raw) {
-  const uint4 u = numbers8(d.seed, d.subsequence, d.first + i);
+  const uint4 u = numbers8(d.gen, d.first + i);
   uint32_t *w = &raw[0].x;
-  const uint32_t n[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const bool lo = (n[j] & 0xffffu) >= d.threshold, hi = (n[j] >> 16) >= d.threshold;
+    const bool lo = kept(u, 2 * j, d.cut), hi = kept(u, 2 * j + 1, d.cut);
     if constexpr (DT == kF32) {
       if (!lo) w[2 * j] = 0;
       if (!hi) w[2 * j + 1] = 0;
@@ -78,17 +77,20 @@ __device__ __forceinline__ void mask8(const DropParams &d, unsigned long long i,
 
 // Eight elements of one block to codes.
 template <bool SR, bool DROP>
-__device__ __forceinline__ uint32_t codes8(float v[8], uint32_t byte, float dscale, unsigned long long seed,
-                                           unsigned long long sub, unsigned long long group) {
-  const float inv = inverse_scale(byte);
+__device__ __forceinline__ uint32_t codes8(float v[8], uint32_t byte, float inv, float dscale, const Generator &gen,
+                                           unsigned long long group) {
+  if constexpr (DROP) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    if constexpr (DROP) v[j] = __fmul_rn(v[j], dscale);
-    v[j] = __fmul_rn(v[j], inv);
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], dscale);
   }
   uint32_t q;
-  if constexpr (SR) q = pack8_stochastic(v, philox(seed, sub, group));
-  else q = pack8_nearest(v);
+  if constexpr (SR) {
+    q = pack8_stochastic(v, byte, inv, philox(gen, group));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
+    q = pack8_nearest(v);
+  }
   return byte == 255u ? 0u : q;
 }
 
@@ -96,54 +98,66 @@ __device__ __forceinline__ uint32_t codes8(float v[8], uint32_t byte, float dsca
 // along the rows
 // --------------------------------------------------------------------------
 
-// One CTA: 128 rows by 256 columns, the extent of one scale tile.  Warp w
-// takes rows w, w + warps, ...; a lane takes eight neighbours of a row (one
-// counter of the generator, one 32-bit word of codes), four lanes a block.
-// The scales gather in shared memory, so the tile is written whole, its
-// padding as zeros.
+// One CTA: 128 rows by 256 columns, the extent of one scale tile.  A lane takes
+// sixteen neighbours, half a block (two counters of the generator, one store
+// of eight bytes), so a warp takes two rows at a time; warp w the pairs w,
+// w + warps, ...  Eight a lane, four lanes a block, took 12 instructions an
+// element instead of 7.  The scales gather in shared memory, so the tile is
+// written whole, its padding as zeros.
 template <int DT, bool SR, bool DROP>
 __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ QuantParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
+  using T = typename Fmt<DT>::type;
+  constexpr int N = 2 * kRaw8<DT>;        // 16-byte loads a lane and row
+  constexpr int U = DT == kF32 ? 2 : 4;   // pairs of rows in flight
   __shared__ __align__(16) uint8_t tile[kMx4TileBytes];
   const Mx4Out &o = p.by_rows;
   const unsigned tk = blockIdx.x % (unsigned)o.tiles_k, tr = blockIdx.x / (unsigned)o.tiles_k;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
-  const long long c0 = (long long)tk * kMx4TileCols + lane * 8, r0 = (long long)tr * kMx4TileRows + warp;
-  const int valid = (int)max(0ll, min(8ll, p.cols - c0));
-  const bool in_row = c0 < o.row_bytes * 2;
-  constexpr int U = 4;  // rows in flight
+  const int cl = lane % 16 * 16, rl0 = warp * 2 + lane / 16;
+  const long long c0 = (long long)tk * kMx4TileCols + cl, r0 = (long long)tr * kMx4TileRows + rl0;
+  const int valid = (int)max(0ll, min(16ll, p.cols - c0));
+  const bool whole = p.vec && valid == 16, in_row = c0 < o.row_bytes * 2;
+  const T *src = static_cast<const T *>(p.x) + r0 * p.ld + c0;
+  uint8_t *dst = o.data + r0 * o.row_bytes + c0 / 2;
+  const long long left = p.rows - r0;     // rows from this lane's first on
 #pragma unroll 1
-  for (int k = 0; k < kMx4TileRows; k += U * warps) {
-    uint4 raw[U][kRaw8<DT>];
+  for (int k = 0; k < kMx4TileRows; k += 2 * U * warps) {
+    uint4 raw[U][N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long r = r0 + k + u * warps;
+      const int dr = k + u * 2 * warps;
 #pragma unroll
-      for (int j = 0; j < kRaw8<DT>; ++j)
-        raw[u][j] = r < p.rows ? load16<DT>(p.x, r * p.ld + c0 + 4 * j, valid - 4 * j, p.vec) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < N; ++j) {
+        if (whole && dr < left) raw[u][j] = ldg_stream(reinterpret_cast<const uint4 *>(src + dr * p.ld) + j);
+        else raw[u][j] = dr < left ? load16<DT>(p.x, (r0 + dr) * p.ld + c0 + j * 16 / (int)sizeof(T), valid - j * 16 / (int)sizeof(T), false) : make_uint4(0, 0, 0, 0);
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const long long r = r0 + k + u * warps;
-      const int rl = warp + k + u * warps;
-      uint32_t byte = 0;
-      if (r < p.rows) {  // the same for the whole warp
-        if constexpr (DROP) mask8<DT>(p.drop, (unsigned long long)(r * p.cols + c0), raw[u]);
-        uint32_t m = max_mag8<DT>(raw[u]);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        m = mag_bits<DT>(m, 0);
-        if constexpr (DROP) m = __float_as_uint(__fmul_rn(__uint_as_float(m), p.drop.scale));
-        byte = scale_byte(m);
-        float v[8];
-        widen8<DT>(raw[u], v);
-        const uint32_t q = codes8<SR, DROP>(v, byte, p.drop.scale, p.seed, p.subsequence,
-                                            (unsigned long long)(r * o.row_bytes * 2 + c0) >> 3);
-        if (in_row) *reinterpret_cast<uint32_t *>(o.data + r * o.row_bytes + c0 / 2) = q;
+      const int dr = k + u * 2 * warps, rl = rl0 + dr;
+      if constexpr (DROP) {
+        const unsigned long long i = (unsigned long long)((r0 + dr) * p.cols + c0);
+        mask8<DT>(p.drop, i, raw[u]);
+        mask8<DT>(p.drop, i + 8, raw[u] + kRaw8<DT>);
       }
-      if ((lane & 3) == 0)
-        tile[(lane >> 4) * kMx4AtomBytes + (rl & 31) * 16 + (rl >> 5) * 4 + ((lane >> 2) & 3)] = (uint8_t)byte;
+      uint32_t m = max(max_mag8<DT>(raw[u]), max_mag8<DT>(raw[u] + kRaw8<DT>));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = mag_bits<DT>(m, 0);
+      if constexpr (DROP) m = __float_as_uint(__fmul_rn(__uint_as_float(m), p.drop.scale));
+      const uint32_t byte = scale_byte(m);
+      const float inv = inverse_scale(byte);
+      const unsigned long long group = (unsigned long long)((r0 + dr) * o.row_bytes * 2 + c0) >> 3;
+      uint2 q;
+      float v[8];
+      widen8<DT>(raw[u], v);
+      q.x = codes8<SR, DROP>(v, byte, inv, p.drop.scale, p.gen_rows, group);
+      widen8<DT>(raw[u] + kRaw8<DT>, v);
+      q.y = codes8<SR, DROP>(v, byte, inv, p.drop.scale, p.gen_rows, group + 1);
+      if (dr < left && in_row) *reinterpret_cast<uint2 *>(dst + dr * o.row_bytes) = q;
+      if ((lane & 1) == 0)
+        tile[(cl >> 7) * kMx4AtomBytes + (rl & 31) * 16 + (rl >> 5) * 4 + ((cl >> 5) & 3)] = (uint8_t)byte;
     }
   }
   __syncthreads();
@@ -230,7 +244,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
         float v[8];
         widen8<DT>(raw, v);
         const long long i = r * o.row_bytes * 2 + c0;
-        const uint32_t q = codes8<SR, DROP>(v, byte, dscale, p.seed, p.subsequence, (unsigned long long)i >> 3);
+        const uint32_t q = codes8<SR, DROP>(v, byte, inverse_scale(byte), dscale, p.gen_rows, (unsigned long long)i >> 3);
         if (r < p.rows && c0 < o.row_bytes * 2) *reinterpret_cast<uint32_t *>(o.data + i / 2) = q;
         if ((lane & 3) == 0) scales_r[cl >> 7][(rl & 31) * 16 + (rl >> 5) * 4 + ((cl >> 5) & 3)] = (uint8_t)byte;
       }
@@ -239,24 +253,26 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
   }
 
   const Mx4Out &o = p.by_cols;
-  const unsigned long long sub = p.subsequence + (ROWS ? 1 : 0);
   const int half = warp & 1, cl = (warp >> 1) * 32 * C + lane * C;  // 64 of the rows; the lane's first column
   uint4 codes[C][2];
 #pragma unroll
   for (int b = 0; b < 2; ++b) {
     const int rl = half * 64 + b * 32;
     uint32_t w[32];
-    uint32_t m = 0;
+    uint32_t m4[4] = {0, 0, 0, 0};  // four chains
 #pragma unroll
     for (int r = 0; r < 32; ++r) {
       w[r] = *reinterpret_cast<const uint32_t *>(x + (rl + r) * kTileRowBytes + cl * Fmt<DT>::bytes);
-      m = max_mag<DT>(m, w[r]);
+      m4[r % 4] = max_mag<DT>(m4[r % 4], w[r]);
     }
+    const uint32_t m = max_mag<DT>(max_mag<DT>(m4[0], m4[1]), max_mag<DT>(m4[2], m4[3]));
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       uint32_t mc = mag_bits<DT>(m, c);
       if constexpr (DROP) mc = __float_as_uint(__fmul_rn(__uint_as_float(mc), dscale));
       const uint32_t byte = scale_byte(mc);
+      const float inv = inverse_scale(byte);
+      const unsigned long long group = (unsigned long long)((col0 + cl + c) * o.row_bytes * 2 + row0 + rl) >> 3;
       uint32_t q[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -268,8 +284,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
           else if constexpr (DT == kBF16) v[e] = __uint_as_float(c ? y & 0xffff0000u : y << 16);
           else v[e] = c ? __high2float(as_h2(y)) : __low2float(as_h2(y));
         }
-        q[g] = codes8<SR, DROP>(v, byte, dscale, p.seed, sub,
-                                (unsigned long long)((col0 + cl + c) * o.row_bytes * 2 + row0 + rl + 8 * g) >> 3);
+        q[g] = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_cols, group + g);
       }
       codes[c][b] = make_uint4(q[0], q[1], q[2], q[3]);
       const int cc = cl + c;
@@ -349,7 +364,7 @@ cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
 
 template <int DT>
 cudaError_t quantize_any(const QuantParams &p, cudaStream_t s) {
-  const bool drop = p.drop.threshold != 0;
+  const bool drop = p.drop.cut != 0;
   if (p.stochastic) return drop ? quantize_dt<DT, true, true>(p, s) : quantize_dt<DT, true, false>(p, s);
   return drop ? quantize_dt<DT, false, true>(p, s) : quantize_dt<DT, false, false>(p, s);
 }

@@ -80,6 +80,7 @@ struct QuantParams {
   Mx4Out by_rows, by_cols;   // data null: not wanted
   Generator gen_rows, gen_cols;  // stochastic rounding
   DropParams drop;
+  uintptr_t x_lo, x_hi;  // the bytes of x: [x_lo, x_hi)
   int dtype, sms;
   bool stochastic;
   bool vec;   // every 16-byte group of a row is aligned

@@ -122,6 +122,7 @@ rr_status ring_mx4_quantize(const void *x, size_t rows, size_t cols, size_t ld, 
   p.dtype = dtype;
   p.stochastic = rounding == RR_MX4_STOCHASTIC;
   p.vec = aligned16(x, rows, ld, E);
+  p.x_lo = sx.lo, p.x_hi = sx.hi;
   unsigned *status;
   const rr_status st = rr::device_info(&status, &p.sms);
   if (st != RR_OK) return st;
@@ -216,8 +217,8 @@ rr_status ring_mx4_allreduce(const rr_mx4 *in, void *const *out_bufs, int R, rr_
     p.data[r] = static_cast<const uint8_t *>(in[r].data);
     p.scales[r] = static_cast<const uint8_t *>(in[r].scales);
     p.out[r] = out_bufs[r];
-    p.vec = p.vec && aligned16(out_bufs[r], rows, cols, E);
-    p.vec32 = p.vec32 && aligned32(out_bufs[r], rows, cols, E);
+    p.vec = p.vec && aligned16(out_bufs[r], 1, cols, E);  // contiguous: one long row
+    p.vec32 = p.vec32 && aligned32(out_bufs[r], 1, cols, E);
   }
   for (int r = 0; r < R; ++r)
     for (int s = 0; s < R; ++s)

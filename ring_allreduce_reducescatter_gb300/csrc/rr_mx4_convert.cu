@@ -165,77 +165,185 @@ __global__ void __launch_bounds__(kFlatThreads) dropout_rows_kernel(const __grid
 }
 
 // --------------------------------------------------------------------------
-// the fold of R ranks' 4-bit matrices
+// the fold of R ranks' 4-bit matrices into contiguous outputs
 // --------------------------------------------------------------------------
 
-// Sixteen values summed over the ranks from rank c on, four ranks' loads in
-// flight.
-__device__ __forceinline__ void fold16(const Mx4ReduceParams &p, int c, long long at, long long sat, float acc[16]) {
-  const int R = p.R;
+// Element i = row * cols + column lies in chunk c of the partition of
+// rows * cols into R chunks and is folded from rank c on, in binary32, as
+// ring_allreduce does on the values; the sum is rounded once to storage.  A
+// thread takes sixteen neighbours of the flat output, so its stores are whole
+// aligned sectors whatever the number of columns; where columns are no
+// multiple of 16 it shifts its codes into place and may meet two scales.  (A
+// thread by sixteen columns of a row instead stored rows of odd length element
+// by element: 46 us for the values of 5003 x 1999, now 14.)  With R = 1 it
+// is the values of one matrix.
+
+// Where the sixteen elements of a thread lie: from column `col` of row `row`
+// on, the first `here` of them in that row, the rest at the start of the next
+// one (cols >= 16).
+struct Group {
+  long long row, col;
+  int here;    // 16: all
+  bool next;   // some lie in the next row
+};
+
+// The sum over the ranks from rank c on, kB ranks' loads in flight.  kAligned:
+// the group is half a block.  Otherwise its codes are shifted into place and
+// its scales are up to three: the block of its first element, the one after
+// it, and the next row's first.
+template <bool kAligned, bool kOne>
+__device__ __forceinline__ void fold16(const Mx4ReduceParams &p, int c, const Group &g, float sum[16]) {
+  constexpr int kB = kOne ? 1 : kAligned ? 4 : 2;
+  const int R = kOne ? 1 : p.R;
+  const long long at = g.row * p.row_bytes + g.col / 8 * 4;
+  const long long sat = scale_offset(g.row, g.col / kMx4Block, p.tiles_k);
+  const int sh = (int)(g.col & 7) * 4, edge = kMx4Block - (int)(g.col & 31);  // edge: first element of the second block
+  const int words = (int)((g.col & 7) + g.here + 7) / 8;                      // of this row's codes
+  const bool two = edge < g.here;
+  const long long sat1 = !kAligned && two ? scale_offset(g.row, g.col / kMx4Block + 1, p.tiles_k) : sat;
+  const long long next = (g.row + 1) * p.row_bytes, snext = g.next ? scale_offset(g.row + 1, 0, p.tiles_k) : sat;
   int k = c;
-  for (int s0 = 0; s0 < R; s0 += 4) {
-    uint2 codes[4];
-    uint8_t byte[4];
+  for (int s0 = 0; s0 < R; s0 += kB) {
+    uint32_t w[kB][3], n[kB][2];
+    uint8_t y[kB][3];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < kB; ++b) {
       if (s0 + b >= R) break;
-      codes[b] = __ldg(reinterpret_cast<const uint2 *>(p.data[k] + at));
-      byte[b] = __ldg(p.scales[k] + sat);
+      const uint32_t *q = reinterpret_cast<const uint32_t *>(p.data[k] + at);
+      if constexpr (kAligned) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(q));
+        w[b][0] = u.x, w[b][1] = u.y;
+      } else {
+        w[b][0] = __ldg(q);
+        w[b][1] = words > 1 ? __ldg(q + 1) : 0u;
+        w[b][2] = words > 2 ? __ldg(q + 2) : 0u;
+        y[b][1] = __ldg(p.scales[k] + sat1);
+        n[b][0] = n[b][1] = 0;
+        y[b][2] = 0;
+        if (g.next) {
+          const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p.data[k] + next));
+          n[b][0] = u.x, n[b][1] = u.y;
+          y[b][2] = __ldg(p.scales[k] + snext);
+        }
+      }
+      y[b][0] = __ldg(p.scales[k] + sat);
       k = k + 1 == R ? 0 : k + 1;
     }
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < kB; ++b) {
       if (s0 + b >= R) break;
-      const float scale = scale_value(byte[b]);
       float v[16];
-      unpack8(codes[b].x, scale, v), unpack8(codes[b].y, scale, v + 8);
+      const float scale = scale_value(y[b][0]);
+      if constexpr (kAligned) {
+        unpack8(w[b][0], scale, v), unpack8(w[b][1], scale, v + 8);
+      } else {
+        // (columns past the last are stored as zeros, so the codes only need joining)
+        uint32_t lo = __funnelshift_r(w[b][0], w[b][1], sh), hi = __funnelshift_r(w[b][1], w[b][2], sh);
+        if (g.next) {
+          const unsigned long long m = (((unsigned long long)n[b][1] << 32) | n[b][0]) << (4 * g.here);
+          lo |= (uint32_t)m, hi |= (uint32_t)(m >> 32);
+        }
+        unpack8(lo, 1.f, v), unpack8(hi, 1.f, v + 8);
+        const float scale1 = scale_value(y[b][1]), scale2 = scale_value(y[b][2]);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) acc[j] = s0 + b == 0 ? v[j] : __fadd_rn(acc[j], v[j]);
+        for (int j = 0; j < 16; ++j) v[j] = __fmul_rn(v[j], j >= g.here ? scale2 : j < edge ? scale : scale1);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sum[j] = s0 + b == 0 ? v[j] : __fadd_rn(sum[j], v[j]);
     }
   }
 }
 
-// Element i = row * cols + column lies in chunk c of the partition of
-// rows * cols into R chunks and is folded from rank c on, in binary32, as
-// ring_allreduce does on the values; the sum is rounded once to storage.
-template <int DT>
-__global__ void __launch_bounds__(kFlatThreads) mx4_reduce_kernel(const __grid_constant__ Mx4ReduceParams p) {
+// A group that meets several chunks: each chunk's fold, an element from its own.
+__device__ __noinline__ void fold_chunks(const Mx4ReduceParams &p, int first, long long i0, int valid, const Group &g,
+                                         float sum[16]) {
+#pragma unroll 1
+  for (int c = first; c < p.R; ++c) {
+    if (c > first && i0 + valid <= c * p.base) break;
+    float more[16];
+    fold16<false, false>(p, c, g, more);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sum[j] = c == first || i0 + j >= c * p.base ? more[j] : sum[j];
+  }
+}
+
+// One element, for rows shorter than sixteen.
+__device__ __noinline__ float fold_element(const Mx4ReduceParams &p, int c, long long row, long long col) {
+  float acc = 0.f;
+  int k = c;
+  for (int s = 0; s < p.R; ++s) {
+    const uint32_t byte = __ldg(p.data[k] + row * p.row_bytes + col / 2);
+    const uint32_t code = (col & 1) ? byte >> 4 : byte & 15u;
+    float v[8];
+    unpack8(code, scale_value(__ldg(p.scales[k] + scale_offset(row, col / kMx4Block, p.tiles_k))), v);
+    acc = s == 0 ? v[0] : __fadd_rn(acc, v[0]);
+    k = k + 1 == p.R ? 0 : k + 1;
+  }
+  return acc;
+}
+
+// kOne: R = 1, the values of one matrix.
+template <int DT, bool kAligned, bool kOne>
+__global__ void __launch_bounds__(kFlatThreads, kAligned || kOne ? 4 : 3) mx4_fold_kernel(const __grid_constant__ Mx4ReduceParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
-  const long long c0 = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 16;
-  const int valid = (int)max(0ll, min(16ll, p.cols - c0));
-  if (valid == 0) return;
-  const int R = p.R;
+  const long long total = p.rows * p.cols, i0 = ((long long)blockIdx.x * kFlatThreads + threadIdx.x) * 16;
+  if (i0 >= total) return;
+  // (a 64-bit division takes several times the instructions of a 32-bit one)
+  const bool narrow = total < (1ll << 32);
   auto chunk = [&](long long i) {
-    if (p.base == 0) return R - 1;
-    // (a 64-bit division takes several times the instructions of a 32-bit one)
-    const long long c = p.rows * p.cols < (1ll << 32) ? (long long)((unsigned)i / (unsigned)p.base) : i / p.base;
-    return c < R - 1 ? (int)c : R - 1;
+    if (kOne || p.base == 0) return p.R - 1;
+    const long long c = narrow ? (long long)((unsigned)i / (unsigned)p.base) : i / p.base;
+    return c < p.R - 1 ? (int)c : p.R - 1;
   };
-  for (long long r = (long long)blockIdx.y * blockDim.y + threadIdx.y; r < p.rows;
-       r += (long long)gridDim.y * blockDim.y) {
-    const long long at = r * p.row_bytes + c0 / 2, sat = scale_offset(r, c0 / kMx4Block, p.tiles_k);
-    const long long i0 = r * p.cols + c0;
+  const int valid = (int)min(16ll, total - i0);
+  Group g;
+  g.row = narrow ? (long long)((unsigned)i0 / (unsigned)p.cols) : i0 / p.cols;
+  g.col = i0 - g.row * p.cols;
+  g.here = kAligned ? 16 : (int)min(16ll, p.cols - g.col);
+  g.next = !kAligned && g.here < 16 && g.row + 1 < p.rows;
+  float sum[16];
+  if (kAligned || p.cols >= 16) {
     const int first = chunk(i0);
-    float sum[16];
-    fold16(p, first, at, sat, sum);
-    if (first + 1 < R && i0 + valid > (first + 1) * p.base) {  // the group ends in another chunk, or several
-      const int last = chunk(i0 + valid - 1);
-      for (int c = first + 1; c <= last; ++c) {
-        float acc[16];
-        fold16(p, c, at, sat, acc);
+    if (kOne || first == p.R - 1 || i0 + valid <= (first + 1) * p.base) fold16<kAligned, kOne>(p, first, g, sum);
+    else {
+      float v[16];  // (in local memory: its address is taken)
+      fold_chunks(p, first, i0, valid, g, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (chunk(i0 + j) == c) sum[j] = acc[j];
-      }
+      for (int j = 0; j < 16; ++j) sum[j] = v[j];
     }
-    for (int k = 0; k < R; ++k) store16<DT>(p.out[k], i0, valid, p.vec, p.vec32, sum);
+  } else {
+    long long r = g.row, c = g.col;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      sum[j] = j < valid ? fold_element(p, chunk(i0 + j), r, c) : 0.f;
+      if (++c == p.cols) c = 0, ++r;
+    }
   }
+  for (int k = 0; k < (kOne ? 1 : p.R); ++k) store16<DT>(p.out[k], i0, valid, p.vec, p.vec32, sum);
+}
+
+template <int DT>
+cudaError_t fold_dt(const Mx4ReduceParams &p, cudaStream_t s) {
+  const long long grid = ceil_div(ceil_div(p.rows * p.cols, 16ll), (long long)kFlatThreads);
+  if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const Shape sh{dim3((unsigned)grid), dim3(kFlatThreads)};
+  if (p.R == 1 && p.cols % 16 != 0) return launch(mx4_fold_kernel<DT, false, true>, sh, p, s);
+  return p.cols % 16 == 0 ? launch(mx4_fold_kernel<DT, true, false>, sh, p, s)
+                          : launch(mx4_fold_kernel<DT, false, false>, sh, p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_dequantize(const DequantParams &p, cudaStream_t s) {
+  if (p.ld == p.cols && p.cols % 16 != 0) {  // contiguous rows of odd length
+    Mx4ReduceParams q{};
+    q.data[0] = p.data, q.scales[0] = p.scales, q.out[0] = p.out;
+    q.rows = p.rows, q.cols = p.cols, q.row_bytes = p.row_bytes, q.tiles_k = p.tiles_k, q.base = p.rows * p.cols;
+    q.R = 1, q.dtype = p.dtype;
+    q.vec = reinterpret_cast<uintptr_t>(p.out) % 16 == 0, q.vec32 = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
+    return launch_mx4_reduce(q, s);
+  }
   const Shape sh = shape_of(p.row_bytes / 8, p.rows, 4);
   return p.dtype == kF32   ? launch(mx4_values_kernel<kF32>, sh, p, s)
          : p.dtype == kF16 ? launch(mx4_values_kernel<kF16>, sh, p, s)
@@ -263,10 +371,7 @@ cudaError_t launch_dropout(const DropoutParams &p, cudaStream_t s) {
 }
 
 cudaError_t launch_mx4_reduce(const Mx4ReduceParams &p, cudaStream_t s) {
-  const Shape sh = shape_of(p.row_bytes / 8, p.rows, 1);
-  return p.dtype == kF32   ? launch(mx4_reduce_kernel<kF32>, sh, p, s)
-         : p.dtype == kF16 ? launch(mx4_reduce_kernel<kF16>, sh, p, s)
-                           : launch(mx4_reduce_kernel<kBF16>, sh, p, s);
+  return p.dtype == kF32 ? fold_dt<kF32>(p, s) : p.dtype == kF16 ? fold_dt<kF16>(p, s) : fold_dt<kBF16>(p, s);
 }
 
 }  // namespace rr

@@ -18,20 +18,46 @@ __device__ __forceinline__ void copy_async16(void *smem_dst, const void *src) {
 }
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Sixteen bytes of storage elements, of which the first `valid` exist.
-template <int DT>
-__device__ __forceinline__ uint4 load16(const void *base, long long at, int valid, bool vec) {
+// Sixteen bytes kN times, neighbouring elements of x from element `at` on, of
+// which the first `valid` exist (the rest read as zero), element by element.
+template <int DT, int kN>
+__device__ __forceinline__ void load_ends(const QuantParams &p, long long at, int valid, uint4 out[kN]) {
   constexpr int E = 16 / Fmt<DT>::bytes;
-  const uint8_t *p = static_cast<const uint8_t *>(base) + at * Fmt<DT>::bytes;
-  if (vec && valid >= E) return ldg_stream(p);
-  uint32_t w[4] = {0, 0, 0, 0};
+  const uint8_t *q = static_cast<const uint8_t *>(p.x) + at * Fmt<DT>::bytes;
 #pragma unroll
-  for (int j = 0; j < E; ++j)
-    if (j < valid) {
-      if constexpr (DT == kF32) w[j] = reinterpret_cast<const uint32_t *>(p)[j];
-      else w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[j] << (16 * (j & 1));
-    }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  for (int n = 0; n < kN; ++n) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (n * E + j < valid) {
+        if constexpr (DT == kF32) w[j] = reinterpret_cast<const uint32_t *>(q)[n * E + j];
+        else w[j / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(q)[n * E + j] << (16 * (j & 1));
+      }
+    out[n] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// The same for rows off the 16-byte grid, in two steps so that several rows'
+// loads can be in flight: the aligned vectors around the elements (where all
+// exist and the vectors lie inside x), then the elements out of them.
+template <int DT, int kN>
+__device__ __forceinline__ bool load_around(const QuantParams &p, long long at, int valid, uint4 v[kN + 1]) {
+  const uintptr_t q = reinterpret_cast<uintptr_t>(p.x) + (uintptr_t)(at * Fmt<DT>::bytes), a = q & ~(uintptr_t)15;
+  if (valid < kN * 16 / Fmt<DT>::bytes || a < p.x_lo || a + 16 * (kN + 1) > p.x_hi) return false;
+#pragma unroll
+  for (int j = 0; j <= kN; ++j) v[j] = ldg_l1(reinterpret_cast<const void *>(a + 16 * j));
+  return true;
+}
+template <int DT, int kN>
+__device__ __forceinline__ void take_from(const QuantParams &p, long long at, int valid, bool around,
+                                          const uint4 v[kN + 1], uint4 out[kN]) {
+  if (around) {
+    const int sh = (int)((reinterpret_cast<uintptr_t>(p.x) + (uintptr_t)(at * Fmt<DT>::bytes)) & 15);
+#pragma unroll
+    for (int j = 0; j < kN; ++j) out[j] = funnel16(v[j], v[j + 1], sh);
+  } else {
+    load_ends<DT, kN>(p, at, valid, out);
+  }
 }
 
 // Running maximum of magnitudes: of the two halves of a word apart for 16-bit
@@ -118,44 +144,48 @@ __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ Q
   const int cl = lane % 16 * 16, rl0 = warp * 2 + lane / 16;
   const long long c0 = (long long)tk * kMx4TileCols + cl, r0 = (long long)tr * kMx4TileRows + rl0;
   const int valid = (int)max(0ll, min(16ll, p.cols - c0));
-  const bool whole = p.vec && valid == 16, in_row = c0 < o.row_bytes * 2;
-  const T *src = static_cast<const T *>(p.x) + r0 * p.ld + c0;
+  const bool in_row = c0 < o.row_bytes * 2;
+  const T *src = static_cast<const T *>(p.x) + r0 * p.ld + c0;  // read only where it exists
   uint8_t *dst = o.data + r0 * o.row_bytes + c0 / 2;
-  const long long left = p.rows - r0;     // rows from this lane's first on
+  const long long left = p.rows - r0;  // rows from this lane's first on
 #pragma unroll 1
   for (int k = 0; k < kMx4TileRows; k += 2 * U * warps) {
     uint4 raw[U][N];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int dr = k + u * 2 * warps;
+      if (valid == 16 && dr < left) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (whole && dr < left) raw[u][j] = ldg_stream(reinterpret_cast<const uint4 *>(src + dr * p.ld) + j);
-        else raw[u][j] = dr < left ? load16<DT>(p.x, (r0 + dr) * p.ld + c0 + j * 16 / (int)sizeof(T), valid - j * 16 / (int)sizeof(T), false) : make_uint4(0, 0, 0, 0);
+        for (int j = 0; j < N; ++j) raw[u][j] = ldg_stream(reinterpret_cast<const uint4 *>(src + dr * p.ld) + j);
+      } else {
+        load_ends<DT, N>(p, (r0 + dr) * p.ld + c0, dr < left ? valid : 0, raw[u]);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int dr = k + u * 2 * warps, rl = rl0 + dr;
-      if constexpr (DROP) {
-        const unsigned long long i = (unsigned long long)((r0 + dr) * p.cols + c0);
-        mask8<DT>(p.drop, i, raw[u]);
-        mask8<DT>(p.drop, i + 8, raw[u] + kRaw8<DT>);
+      uint32_t byte = 0;
+      if (dr < left + lane / 16) {  // the warp's first row exists
+        if constexpr (DROP) {
+          const unsigned long long i = (unsigned long long)((r0 + dr) * p.cols + c0);
+          mask8<DT>(p.drop, i, raw[u]);
+          mask8<DT>(p.drop, i + 8, raw[u] + kRaw8<DT>);
+        }
+        uint32_t m = max(max_mag8<DT>(raw[u]), max_mag8<DT>(raw[u] + kRaw8<DT>));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = mag_bits<DT>(m, 0);
+        if constexpr (DROP) m = __float_as_uint(__fmul_rn(__uint_as_float(m), p.drop.scale));
+        byte = scale_byte(m);
+        const float inv = inverse_scale(byte);
+        const unsigned long long group = (unsigned long long)((r0 + dr) * o.row_bytes * 2 + c0) >> 3;
+        uint2 q;
+        float v[8];
+        widen8<DT>(raw[u], v);
+        q.x = codes8<SR, DROP>(v, byte, inv, p.drop.scale, p.gen_rows, group);
+        widen8<DT>(raw[u] + kRaw8<DT>, v);
+        q.y = codes8<SR, DROP>(v, byte, inv, p.drop.scale, p.gen_rows, group + 1);
+        if (dr < left && in_row) *reinterpret_cast<uint2 *>(dst + dr * o.row_bytes) = q;
       }
-      uint32_t m = max(max_mag8<DT>(raw[u]), max_mag8<DT>(raw[u] + kRaw8<DT>));
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      m = mag_bits<DT>(m, 0);
-      if constexpr (DROP) m = __float_as_uint(__fmul_rn(__uint_as_float(m), p.drop.scale));
-      const uint32_t byte = scale_byte(m);
-      const float inv = inverse_scale(byte);
-      const unsigned long long group = (unsigned long long)((r0 + dr) * o.row_bytes * 2 + c0) >> 3;
-      uint2 q;
-      float v[8];
-      widen8<DT>(raw[u], v);
-      q.x = codes8<SR, DROP>(v, byte, inv, p.drop.scale, p.gen_rows, group);
-      widen8<DT>(raw[u] + kRaw8<DT>, v);
-      q.y = codes8<SR, DROP>(v, byte, inv, p.drop.scale, p.gen_rows, group + 1);
-      if (dr < left && in_row) *reinterpret_cast<uint2 *>(dst + dr * o.row_bytes) = q;
       if ((lane & 1) == 0)
         tile[(cl >> 7) * kMx4AtomBytes + (rl & 31) * 16 + (rl >> 5) * 4 + ((cl >> 5) & 3)] = (uint8_t)byte;
     }
@@ -172,7 +202,7 @@ __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ Q
 
 // One CTA: 128 rows by W columns (512 bytes a row), brought to shared memory
 // by asynchronous copies, three CTAs an SM, so that one's loads run under
-// another's arithmetic.  First the rows (a lane eight neighbours, four lanes a
+// another's arithmetic.  First the rows (a lane sixteen neighbours, two lanes a
 // block; dropout is applied in place here), then the columns: a lane takes the
 // 32-bit word of one column, or two, down 32 rows, a whole block in
 // registers, two blocks one after the other, 32 bytes of codes.  (Holding the
@@ -182,7 +212,7 @@ constexpr int kTileThreads = 256;
 constexpr int kTileRowBytes = 512;
 constexpr int kTileSmem = kMx4TileRows * kTileRowBytes;
 
-template <int DT, bool SR, bool DROP, bool ROWS>
+template <int DT, bool SR, bool DROP, bool ROWS, bool COLS>
 __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_constant__ QuantParams p,
                                                                   unsigned tiles_c, bool out32) {
   grid_dependency_wait();
@@ -201,116 +231,152 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
   {
     const int c = (threadIdx.x % 32) * E;
     const int valid = (int)max(0ll, min((long long)E, p.cols - col0 - c));
+    unsigned char *dst = x + warp * kTileRowBytes + (threadIdx.x % 32) * 16;
+    const long long at = (row0 + warp) * p.ld + col0 + c;
+    const long long left = p.rows - row0 - warp;  // rows from this warp's first on
+    if (p.vec && valid == E) {
 #pragma unroll
-    for (int k = 0; k < kMx4TileRows / 8; ++k) {
-      const int r = warp + 8 * k;
-      unsigned char *dst = x + r * kTileRowBytes + (threadIdx.x % 32) * 16;
-      const long long at = (row0 + r) * p.ld + col0 + c;
-      if (row0 + r < p.rows && p.vec && valid == E)
-        copy_async16(dst, static_cast<const uint8_t *>(p.x) + at * Fmt<DT>::bytes);
-      else
-        *reinterpret_cast<uint4 *>(dst) =
-            row0 + r < p.rows ? load16<DT>(p.x, at, valid, false) : make_uint4(0, 0, 0, 0);
+      for (int k = 0; k < kMx4TileRows; k += 8) {
+        if (k < left)
+          copy_async16(dst + k * kTileRowBytes, static_cast<const uint8_t *>(p.x) + (at + k * p.ld) * Fmt<DT>::bytes);
+        else
+          *reinterpret_cast<uint4 *>(dst + k * kTileRowBytes) = make_uint4(0, 0, 0, 0);
+      }
+    } else {
+      constexpr int U = 4;
+#pragma unroll 1
+      for (int k = 0; k < kMx4TileRows; k += 8 * U) {
+        uint4 v[U][2], out[U];
+        bool around[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          around[u] = load_around<DT, 1>(p, at + (k + 8 * u) * p.ld, k + 8 * u < left ? valid : 0, v[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          take_from<DT, 1>(p, at + (k + 8 * u) * p.ld, k + 8 * u < left ? valid : 0, around[u], v[u], &out[u]);
+          *reinterpret_cast<uint4 *>(dst + (k + 8 * u) * kTileRowBytes) = out[u];
+        }
+      }
     }
     copy_async_wait();
   }
   __syncthreads();
 
   if constexpr (ROWS || DROP) {
-    constexpr int L = W / 8;  // lanes a row
+    constexpr int L = W / 16;  // lanes a row, sixteen neighbours each
+    constexpr int N = 2 * kRaw8<DT>;
     const Mx4Out &o = p.by_rows;
-    const int cl = lane % L * 8;
+    const int cl = lane % L * 16;
     const long long c0 = col0 + cl;
-#pragma unroll 2
+#pragma unroll 1
     for (int k = 0; k < 16; k += 32 / L) {
       const int rl = warp * 16 + k + lane / L;
       const long long r = row0 + rl;
-      uint4 raw[kRaw8<DT>];
+      if (row0 + warp * 16 + k >= p.rows) {  // none of the warp's rows exist
+        if (ROWS && (lane & 1) == 0) scales_r[cl >> 7][(rl & 31) * 16 + (rl >> 5) * 4 + ((cl >> 5) & 3)] = 0;
+        continue;
+      }
+      uint4 raw[N];
       uint4 *at = reinterpret_cast<uint4 *>(x + rl * kTileRowBytes + cl * Fmt<DT>::bytes);
 #pragma unroll
-      for (int j = 0; j < kRaw8<DT>; ++j) raw[j] = at[j];
+      for (int j = 0; j < N; ++j) raw[j] = at[j];
       if constexpr (DROP) {
-        mask8<DT>(p.drop, (unsigned long long)(r * p.cols + c0), raw);
+        const unsigned long long i = (unsigned long long)(r * p.cols + c0);
+        mask8<DT>(p.drop, i, raw);
+        mask8<DT>(p.drop, i + 8, raw + kRaw8<DT>);
 #pragma unroll
-        for (int j = 0; j < kRaw8<DT>; ++j) at[j] = raw[j];
+        for (int j = 0; j < N; ++j) at[j] = raw[j];
       }
       if constexpr (ROWS) {
-        uint32_t m = max_mag8<DT>(raw);
+        uint32_t m = max(max_mag8<DT>(raw), max_mag8<DT>(raw + kRaw8<DT>));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
         m = mag_bits<DT>(m, 0);
         if constexpr (DROP) m = __float_as_uint(__fmul_rn(__uint_as_float(m), dscale));
         const uint32_t byte = scale_byte(m);
+        const float inv = inverse_scale(byte);
+        const long long i = r * o.row_bytes * 2 + c0;
+        uint2 q;
         float v[8];
         widen8<DT>(raw, v);
-        const long long i = r * o.row_bytes * 2 + c0;
-        const uint32_t q = codes8<SR, DROP>(v, byte, inverse_scale(byte), dscale, p.gen_rows, (unsigned long long)i >> 3);
-        if (r < p.rows && c0 < o.row_bytes * 2) *reinterpret_cast<uint32_t *>(o.data + i / 2) = q;
-        if ((lane & 3) == 0) scales_r[cl >> 7][(rl & 31) * 16 + (rl >> 5) * 4 + ((cl >> 5) & 3)] = (uint8_t)byte;
+        q.x = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_rows, (unsigned long long)i >> 3);
+        widen8<DT>(raw + kRaw8<DT>, v);
+        q.y = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_rows, ((unsigned long long)i >> 3) + 1);
+        if (r < p.rows && c0 < o.row_bytes * 2) *reinterpret_cast<uint2 *>(o.data + i / 2) = q;
+        if ((lane & 1) == 0) scales_r[cl >> 7][(rl & 31) * 16 + (rl >> 5) * 4 + ((cl >> 5) & 3)] = (uint8_t)byte;
       }
     }
-    if constexpr (DROP) __syncthreads();
+    if constexpr (DROP && COLS) __syncthreads();
   }
 
-  const Mx4Out &o = p.by_cols;
-  const int half = warp & 1, cl = (warp >> 1) * 32 * C + lane * C;  // 64 of the rows; the lane's first column
-  uint4 codes[C][2];
+  if constexpr (COLS) {
+    const Mx4Out &o = p.by_cols;
+    const int half = warp & 1, cl = (warp >> 1) * 32 * C + lane * C;  // 64 of the rows; the lane's first column
+    uint4 codes[C][2];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    const int rl = half * 64 + b * 32;
-    uint32_t w[32];
-    uint32_t m4[4] = {0, 0, 0, 0};  // four chains
+    for (int b = 0; b < 2; ++b) {
+      const int rl = half * 64 + b * 32;
+      if (row0 + rl >= p.rows) {  // no such block
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-      w[r] = *reinterpret_cast<const uint32_t *>(x + (rl + r) * kTileRowBytes + cl * Fmt<DT>::bytes);
-      m4[r % 4] = max_mag<DT>(m4[r % 4], w[r]);
+        for (int c = 0; c < C; ++c) scales_c[(cl + c) >> 7][((cl + c) & 31) * 16 + (((cl + c) >> 5) & 3) * 4 + half * 2 + b] = 0;
+        continue;
+      }
+      uint32_t w[32];
+      uint32_t m4[4] = {0, 0, 0, 0};  // four chains
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        w[r] = *reinterpret_cast<const uint32_t *>(x + (rl + r) * kTileRowBytes + cl * Fmt<DT>::bytes);
+        m4[r % 4] = max_mag<DT>(m4[r % 4], w[r]);
+      }
+      const uint32_t m = max_mag<DT>(max_mag<DT>(m4[0], m4[1]), max_mag<DT>(m4[2], m4[3]));
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        uint32_t mc = mag_bits<DT>(m, c);
+        if constexpr (DROP) mc = __float_as_uint(__fmul_rn(__uint_as_float(mc), dscale));
+        const uint32_t byte = scale_byte(mc);
+        const float inv = inverse_scale(byte);
+        const unsigned long long group = (unsigned long long)((col0 + cl + c) * o.row_bytes * 2 + row0 + rl) >> 3;
+        uint32_t q[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t y = w[8 * g + e];
+            if constexpr (DT == kF32) v[e] = __uint_as_float(y);
+            else if constexpr (DT == kBF16) v[e] = __uint_as_float(c ? y & 0xffff0000u : y << 16);
+            else v[e] = c ? __high2float(as_h2(y)) : __low2float(as_h2(y));
+          }
+          q[g] = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_cols, group + g);
+        }
+        codes[c][b] = make_uint4(q[0], q[1], q[2], q[3]);
+        const int cc = cl + c;
+        scales_c[cc >> 7][(cc & 31) * 16 + ((cc >> 5) & 3) * 4 + half * 2 + b] = (uint8_t)byte;
+      }
     }
-    const uint32_t m = max_mag<DT>(max_mag<DT>(m4[0], m4[1]), max_mag<DT>(m4[2], m4[3]));
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      uint32_t mc = mag_bits<DT>(m, c);
-      if constexpr (DROP) mc = __float_as_uint(__fmul_rn(__uint_as_float(mc), dscale));
-      const uint32_t byte = scale_byte(mc);
-      const float inv = inverse_scale(byte);
-      const unsigned long long group = (unsigned long long)((col0 + cl + c) * o.row_bytes * 2 + row0 + rl) >> 3;
-      uint32_t q[4];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t y = w[8 * g + e];
-          if constexpr (DT == kF32) v[e] = __uint_as_float(y);
-          else if constexpr (DT == kBF16) v[e] = __uint_as_float(c ? y & 0xffff0000u : y << 16);
-          else v[e] = c ? __high2float(as_h2(y)) : __low2float(as_h2(y));
-        }
-        q[g] = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_cols, group + g);
+      const long long col = col0 + cl + c, row = row0 + half * 64;
+      if (col >= p.cols || row >= p.rows) continue;
+      uint8_t *q = o.data + col * o.row_bytes + row / 2;
+      if (out32 && row + 32 < p.rows) {
+        stg32(q, codes[c][0], codes[c][1]);
+      } else {
+        *reinterpret_cast<uint4 *>(q) = codes[c][0];
+        if (row + 32 < p.rows) *reinterpret_cast<uint4 *>(q + 16) = codes[c][1];
       }
-      codes[c][b] = make_uint4(q[0], q[1], q[2], q[3]);
-      const int cc = cl + c;
-      scales_c[cc >> 7][(cc & 31) * 16 + ((cc >> 5) & 3) * 4 + half * 2 + b] = (uint8_t)byte;
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const long long col = col0 + cl + c, row = row0 + half * 64;
-    if (col >= p.cols || row >= p.rows) continue;
-    uint8_t *q = o.data + col * o.row_bytes + row / 2;
-    if (out32 && row + 32 < p.rows) {
-      stg32(q, codes[c][0], codes[c][1]);
-    } else {
-      *reinterpret_cast<uint4 *>(q) = codes[c][0];
-      if (row + 32 < p.rows) *reinterpret_cast<uint4 *>(q + 16) = codes[c][1];
     }
   }
   __syncthreads();
   // the scales: an atom is 128 columns by this CTA's four blocks
   for (int k = threadIdx.x; k < W / 128 * (kMx4AtomBytes / 16); k += kTileThreads) {
     const int a = k / (kMx4AtomBytes / 16), w = k % (kMx4AtomBytes / 16);
-    const long long rb = (long long)tc * (W / 128) + a;  // 128 rows of the result
-    if (rb * kMx4TileRows < p.cols)
-      reinterpret_cast<uint4 *>(o.scales + (rb * o.tiles_k + tr / 2) * kMx4TileBytes + (tr & 1) * kMx4AtomBytes)[w] =
-          reinterpret_cast<const uint4 *>(scales_c[a])[w];
+    if constexpr (COLS) {
+      const Mx4Out &q = p.by_cols;
+      const long long rb = (long long)tc * (W / 128) + a;  // 128 rows of the result
+      if (rb * kMx4TileRows < p.cols)
+        reinterpret_cast<uint4 *>(q.scales + (rb * q.tiles_k + tr / 2) * kMx4TileBytes + (tr & 1) * kMx4AtomBytes)[w] =
+            reinterpret_cast<const uint4 *>(scales_c[a])[w];
+    }
     if constexpr (ROWS) {
       const Mx4Out &q = p.by_rows;
       const long long atom = (long long)tc * (W / 128) + a;  // 128 columns
@@ -343,23 +409,26 @@ cudaError_t launch(long long grid, int threads, int smem, cudaStream_t s, const 
 
 template <int DT, bool SR, bool DROP>
 cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
-  if (!p.by_cols.data) {
+  const bool rows = p.by_rows.data, cols = p.by_cols.data;
+  if (!cols && p.vec) {
     const long long grid = ceil_div(p.rows, (long long)kMx4TileRows) * p.by_rows.tiles_k;
     // few tiles: more warps share a tile's rows (64 x 4096 is 16 tiles)
     const int threads = grid >= 2ll * p.sms ? 128 : 512;
     return launch<mx4_rows_kernel<DT, SR, DROP>>(grid, threads, 0, s, p);
   }
-  // an even number of tiles of 128 rows (a scale tile of the result spans 256
-  // rows), and columns to whole scale tiles of both results
+  // rows off the 16-byte grid go through the tiles too (binary32 5003 x 1999
+  // along its rows: 26 us element by element a lane)
   constexpr int W = kTileRowBytes / Fmt<DT>::bytes;
-  const long long tiles_r = 2 * p.by_cols.tiles_k;
+  // tiles of 128 rows, an even number of them for the columns (a scale tile of
+  // that result spans 256 rows), and columns to whole scale tiles
+  const long long tiles_r = cols ? 2 * p.by_cols.tiles_k : ceil_div(p.rows, (long long)kMx4TileRows);
   const long long tiles_c = ceil_div(p.cols, (long long)kMx4TileCols) * (kMx4TileCols / W);
   const bool out32 = (reinterpret_cast<uintptr_t>(p.by_cols.data) | (uintptr_t)p.by_cols.row_bytes) % 32 == 0;
-  if (p.by_rows.data)
-    return launch<mx4_tile_kernel<DT, SR, DROP, true>>(tiles_r * tiles_c, kTileThreads, kTileSmem, s, p,
-                                                       (unsigned)tiles_c, out32);
-  return launch<mx4_tile_kernel<DT, SR, DROP, false>>(tiles_r * tiles_c, kTileThreads, kTileSmem, s, p,
-                                                      (unsigned)tiles_c, out32);
+  const long long grid = tiles_r * tiles_c;
+  const unsigned tc = (unsigned)tiles_c;
+  if (!cols) return launch<mx4_tile_kernel<DT, SR, DROP, true, false>>(grid, kTileThreads, kTileSmem, s, p, tc, out32);
+  if (rows) return launch<mx4_tile_kernel<DT, SR, DROP, true, true>>(grid, kTileThreads, kTileSmem, s, p, tc, out32);
+  return launch<mx4_tile_kernel<DT, SR, DROP, false, true>>(grid, kTileThreads, kTileSmem, s, p, tc, out32);
 }
 
 template <int DT>

@@ -113,19 +113,22 @@ __device__ __forceinline__ void finish_ragged(const MatmulKernelParams &p, long 
   for (int j = 0; j < 16; ++j) stage[lane * 17 + j] = v[j];
   __syncwarp();
   const long long c = col + lane % 16, r0 = rows0 + lane / 16;
-  const bool in = c < p.n;
-  float w[16];
+  const int left = c < p.n ? (int)min(32ll, p.m - r0) : 0;  // rows from r0 on
+  const float *from = stage + lane / 16 * 17 + lane % 16;
+  T *o = static_cast<T *>(p.out) + r0 * p.ld_out + c;
+  const long long step = 2 * p.ld_out;
   if (p.residual) {
     const T *q = static_cast<const T *>(p.residual) + r0 * p.ld_res + c;
+    T w[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) w[k] = in && r0 + 2 * k < p.m ? to_f32<DT>(q[2 * k * p.ld_res]) : 0.f;
-  }
-  T *o = static_cast<T *>(p.out) + r0 * p.ld_out + c;
+    for (int k = 0; k < 16; ++k, q += 2 * p.ld_res) w[k] = 2 * k < left ? *q : from_f32<DT>(0.f);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    float x = stage[(2 * k + lane / 16) * 17 + lane % 16];
-    if (p.residual) x = __fadd_rn(w[k], x);
-    if (in && r0 + 2 * k < p.m) o[2 * k * p.ld_out] = from_f32<DT>(x);
+    for (int k = 0; k < 16; ++k, o += step)
+      if (2 * k < left) *o = from_f32<DT>(__fadd_rn(to_f32<DT>(w[k]), from[2 * k * 17]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k, o += step)
+      if (2 * k < left) *o = from_f32<DT>(from[2 * k * 17]);
   }
   __syncwarp();
 }
@@ -162,82 +165,79 @@ __device__ __forceinline__ void finish1(const MatmulKernelParams &p, long long r
 // --------------------------------------------------------------------------
 
 // A cluster of S CTAs computes one tile of 128 rows of P by BN rows of Q, each
-// CTA a contiguous part of K; the parts meet in shared memory, where CTA r adds
-// its share of the columns over all CTAs in rank order (so the result does not
-// depend on timing) and finishes it.  Reading the operands bounds these
-// products, and a grid of whole tiles would leave most SMs without a share of
-// the memory; S is the largest split that still fits the GPU at two CTAs an SM.
+// CTA a contiguous part of K.  Each CTA sends its sums, a group of columns to
+// each CTA in turn, to a place of its own in that CTA's shared memory; one
+// barrier later every CTA adds up the groups it received, in rank order (so
+// the result does not depend on timing), and finishes them.  Reading the
+// operands bounds these products, and a grid of whole tiles would leave most
+// SMs without a share of the memory; S is the largest split that still fits the
+// GPU at two CTAs an SM.  (Reading the other CTAs' sums instead of sending them
+// took a second barrier and the latency of a remote load: 33 rows by 4096 by
+// 11008 took 9.3 us.)
 // kSwap: P is B (a weight matrix, 128 rows a tile) and Q is A (the few tokens
 // of a small batch, BN of them): no operand row is padded beyond BN tokens.
-constexpr int kSplitThreads = 192;  // warps 0-3 epilogue, 4 copies, 5 products
 
 template <int BN>
 struct Split {
   static constexpr int kStageBytes = kHalfBytes + BN * kRowBytes + 2 * kMx4TileBytes;
-  static constexpr int kStages = BN <= 32 ? 5 : BN == 64 ? 4 : 3;  // about 104 KB: two CTAs an SM
-  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+  static constexpr int kStages = BN <= 32 ? 4 : 3;  // two CTAs an SM, with the groups of a split
+  static constexpr int kGroup = BN <= 64 ? 4 : 16;                 // columns a group
+  static constexpr int kGroups = BN / kGroup;
+  // epilogue warps first (four quarters of the rows, once or, each with every
+  // second 16 columns, twice), then one for the copies and one for the products
+  static constexpr int kHalves = BN <= 32 ? 1 : 2;
+  static constexpr int kEpilogue = 4 * kHalves;
+  static constexpr int kThreads = 32 * (kEpilogue + 2);
+  static constexpr int kGroupBytes = kGroup * 128 * 4;
+  // the stages, then the groups received: [split][slots][kGroup / 4][128][4]
+  static __host__ __device__ constexpr int slots(int split) { return (kGroups + split - 1) / split; }
+  static __host__ __device__ constexpr int smem_bytes(int split) {
+    return 1024 + kStages * kStageBytes + (split > 1 ? split * slots(split) * kGroupBytes : 0);
+  }
   static constexpr uint32_t kScales = BN;                          // first column of the scales
   static constexpr uint32_t kColumns = BN <= 64 ? 128 : 256;       // accumulators and the scales of every stage
   static_assert(kScales + kStages * 16 <= kColumns, "they fit");
-  static_assert(kStages * kStageBytes >= 128 * BN * 4 + 4 * kStageFloats * 4, "a part of a tile fits the stages");
+  static_assert(kStages * kStageBytes >= kEpilogue * kStageFloats * 4, "the ragged epilogue fits the stages");
 };
 
-// The sums over the S parts of kV neighbouring columns of this thread's row,
-// kN groups of them, from column c on: every load is issued before the first
-// sum, since another CTA's shared memory is about a microsecond away.
-template <int S, int kV, int kN>
-__device__ __forceinline__ void add_parts(const float *part, int c, int row, float v[kN * kV]) {
-  float4 w[S][kN];
+// The groups of columns that this CTA received, added up and finished.
+template <int DT, int BN, bool kSwap>
+__device__ __forceinline__ void finish_split(const MatmulKernelParams &p, const float *got, int split, int rank, int row,
+                                             int half, long long prow, long long q0, float *stage) {
+  using L = Split<BN>;
+  const int slots = L::slots(split);
+  for (int slot = half, g = rank + half * split; g < L::kGroups; slot += L::kHalves, g += split * L::kHalves) {
+    const long long col = q0 + g * L::kGroup;
+    if (kSwap && col >= p.m) break;
+    float v[L::kGroup];
 #pragma unroll
-  for (int r = 0; r < S; ++r)
+    for (int j = 0; j < L::kGroup; ++j) v[j] = 0.f;
+#pragma unroll 2
+    for (int r = 0; r < split; ++r) {
+      const float4 *w = reinterpret_cast<const float4 *>(got + (r * slots + slot) * (L::kGroup * 128)) + row;
 #pragma unroll
-    for (int n = 0; n < kN; ++n) {
-      // columns 4 g .. 4 g + 3 of a row are 16 bytes, rows follow one another
-      const int col = c + n * kV;
-      const uint32_t at = cluster_addr(part + (col / 4 * 128 + row) * 4 + col % 4, r);
-      w[r][n] = kV == 4 ? cluster_load4(at) : cluster_load2(at);
+      for (int j = 0; j < L::kGroup; j += 4) {
+        const float4 x = w[j / 4 * 128];
+        v[j] = r == 0 ? x.x : __fadd_rn(v[j], x.x);
+        v[j + 1] = r == 0 ? x.y : __fadd_rn(v[j + 1], x.y);
+        v[j + 2] = r == 0 ? x.z : __fadd_rn(v[j + 2], x.z);
+        v[j + 3] = r == 0 ? x.w : __fadd_rn(v[j + 3], x.w);
+      }
     }
+    if constexpr (kSwap) {
 #pragma unroll
-  for (int n = 0; n < kN; ++n) {
-#pragma unroll
-    for (int r = 0; r < S; ++r) {
-      const float *x = &w[r][n].x;
-#pragma unroll
-      for (int j = 0; j < kV; ++j) v[n * kV + j] = r == 0 ? x[j] : __fadd_rn(v[n * kV + j], x[j]);
-    }
-  }
-}
-
-// This CTA's share of the columns of a split tile, added up and finished.
-template <int DT, int BN, bool kSwap, int S>
-__device__ __forceinline__ void finish_split(const MatmulKernelParams &p, const float *part, int rank, int row,
-                                             long long prow, long long q0, float *stage) {
-  constexpr int kShare = BN / S;
-  const int c0 = rank * kShare;
-  if constexpr (kSwap) {
-    constexpr int kV = kShare < 4 ? 2 : 4, kN = kShare / kV < 4 ? kShare / kV : 4;
-#pragma unroll 1
-    for (int c = c0; c < c0 + kShare && q0 + c < p.m; c += kN * kV) {
-      float v[kN * kV];
-      add_parts<S, kV, kN>(part, c, row, v);
-#pragma unroll
-      for (int j = 0; j < kN * kV; ++j) finish1<DT>(p, q0 + c + j, prow, v[j]);
-    }
-  } else {
-#pragma unroll 1
-    for (int c = c0; c < c0 + kShare; c += 16) {
-      float v[16];
-      add_parts<S, 4, 4>(part, c, row, v);
+      for (int j = 0; j < L::kGroup; ++j) finish1<DT>(p, col + j, prow, v[j]);
+    } else {
       uint32_t acc[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) acc[j] = __float_as_uint(v[j]);
-      finish16<DT>(p, prow, q0 + c, acc, stage);
+      for (int j = 0; j < 16; ++j) acc[j] = __float_as_uint(v[j % L::kGroup]);
+      finish16<DT>(p, prow, col, acc, stage);
     }
   }
 }
 
 template <int DT, int BN, bool kSwap>
-__global__ void __launch_bounds__(kSplitThreads, 2) mx4_split_kernel(const __grid_constant__ MatmulKernelParams p,
+__global__ void __launch_bounds__(Split<BN>::kThreads, 2) mx4_split_kernel(const __grid_constant__ MatmulKernelParams p,
                                                                     int split) {
   using L = Split<BN>;
   extern __shared__ unsigned char smem_raw[];
@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mx4_split_kernel(const __gri
     failed = 0;
     fence_mbar_init();
   }
-  if (warp == 5) tmem_alloc<1>(&tmem_slot, L::kColumns);
+  if (split > 1) cluster_arrive();  // waited for before the first remote store: by then every CTA runs
+  if (warp == L::kEpilogue + 1) tmem_alloc<1>(&tmem_slot, L::kColumns);
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mx4_split_kernel(const __gri
   grid_dependency_wait();
   grid_dependents_launch();
 
-  if (warp == 4) {
+  if (warp == L::kEpilogue) {
     const uint64_t pol = l2_evict_normal_policy();
     const bool one = elect_one();
     int k = 0;
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mx4_split_kernel(const __gri
       for (int q = k > L::kStages ? k - L::kStages : 0; q < k; ++q)
         mbar_wait_bounded(&full[q % L::kStages], (q / L::kStages) & 1, kWaitLimitNs);
     }
-  } else if (warp == 5) {
+  } else if (warp == L::kEpilogue + 1) {
     const bool one = elect_one();
     int k = 0;
     for (; k < n_steps; ++k) {
@@ -333,15 +334,18 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mx4_split_kernel(const __gri
   tcgen05_fence_after();
   __syncthreads();
 
-  const int row = warp * 32 + lane;  // of the tile (warps 0-3)
-  const long long prow = (long long)tp * 128 + row;
-  float *part = reinterpret_cast<float *>(smem);  // [BN / 4][128][4]
-  float *stage = part + BN * 128 + warp * kStageFloats;
-  if (warp < 4) {
+  const int row = warp % 4 * 32 + lane, half = warp / 4;  // of the tile (epilogue warps)
+  const long long prow = (long long)tp * 128 + row, q0 = (long long)tq * BN;
+  float *stage = reinterpret_cast<float *>(smem) + warp % L::kEpilogue * kStageFloats;
+  float *got = reinterpret_cast<float *>(smem + L::kStages * L::kStageBytes);
+  if (split > 1) cluster_wait();
+  if (warp < L::kEpilogue) {
+    const int slots = L::slots(split);
 #pragma unroll 1
-    for (int c = 0; c < BN; c += 16) {
+    for (int c = 16 * half; c < BN; c += 16 * L::kHalves) {
+      if (kSwap && q0 + c >= p.m) break;
       uint32_t acc[16];
-      tmem_load16(tmem + ((uint32_t)(warp * 32) << 16) + c, acc);
+      tmem_load16(tmem + ((uint32_t)(warp % 4 * 32) << 16) + c, acc);
       tmem_load_wait();
       if (n_steps == 0) {
 #pragma unroll
@@ -349,32 +353,31 @@ __global__ void __launch_bounds__(kSplitThreads, 2) mx4_split_kernel(const __gri
       }
       if (split > 1) {
 #pragma unroll
-        for (int j = 0; j < 16; j += 4)
-          *reinterpret_cast<uint4 *>(part + ((c + j) / 4 * 128 + row) * 4) = make_uint4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+        for (int j = 0; j < 16; j += 4) {
+          const int g = (c + j) / L::kGroup;
+          if (kSwap && q0 + c + j >= p.m) break;
+          const float *to = got + (rank * slots + g / split) * (L::kGroup * 128) + (((c + j) % L::kGroup) / 4 * 128 + row) * 4;
+          cluster_store4(cluster_addr(to, g % split), make_uint4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
+        }
       } else if (!failed) {
         if constexpr (kSwap) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) finish1<DT>(p, (long long)tq * BN + c + j, prow, __uint_as_float(acc[j]));
+          for (int j = 0; j < 16; ++j) finish1<DT>(p, q0 + c + j, prow, __uint_as_float(acc[j]));
         } else {
-          finish16<DT>(p, prow, (long long)tq * BN + c, acc, stage);
+          finish16<DT>(p, prow, q0 + c, acc, stage);
         }
       }
-    }
-  }
-  if (split > 1) {
-    cluster_sync_all();
-    if (warp < 4 && !failed) {
-      const long long q0 = (long long)tq * BN;
-      if (split == 2) finish_split<DT, BN, kSwap, 2>(p, part, rank, row, prow, q0, stage);
-      else if (split == 4) finish_split<DT, BN, kSwap, 4>(p, part, rank, row, prow, q0, stage);
-      else finish_split<DT, BN, kSwap, 8>(p, part, rank, row, prow, q0, stage);
     }
   }
   tcgen05_fence_before();
   __syncthreads();
   tcgen05_fence_after();
-  if (warp == 5) tmem_free<1>(tmem, L::kColumns);
-  if (split > 1) cluster_sync_all();  // no CTA leaves while another reads its part
+  if (split > 1) cluster_arrive();
+  if (warp == L::kEpilogue + 1) tmem_free<1>(tmem, L::kColumns);
+  if (split > 1) {
+    cluster_wait();
+    if (warp < L::kEpilogue && !failed) finish_split<DT, BN, kSwap>(p, got, split, rank, row, half, prow, q0, stage);
+  }
 }
 
 // --------------------------------------------------------------------------
@@ -581,12 +584,14 @@ bool make_scale_map(CUtensorMap *map, const uint8_t *scales, long long tiles) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr int kMaxSmem = 227 * 1024 - 1024;  // a CTA's dynamic shared memory at most, less its static part
+
 // cluster: CTAs a cluster (given as a launch attribute where the kernel has no
 // size of its own).
 template <auto kKernel, class... Args>
 cudaError_t launch_matmul(long long grid, int threads, int smem, int cluster, cudaStream_t s, const Args &...args) {
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = allow_smem<kKernel>(smem);
+  const cudaError_t e = allow_smem<kKernel>(kMaxSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)grid);
@@ -606,15 +611,18 @@ cudaError_t launch_matmul(long long grid, int threads, int smem, int cluster, cu
 // CTAs a tile.  Up to 64 columns: as many as fit the GPU at two an SM, each with
 // a step or more (1 x 4096 x 4096: 10.1 us whole, 7.8, 6.2 and 5.9 us at 2, 4
 // and 8; 1 x 11008 x 4096, 86 tiles: 10.8, 9.7 and, past two an SM, 12.9 and
-// 16.2 us).  At 128 columns a part is 64 KB to exchange, so at most one CTA an
-// SM and four steps or more each (128 x 4096 x 4096: 11.6, 9.8, 8.8 and 12.8
-// us; 1024^3, 64 tiles of four steps: 6.4 us whole, 7.2 in two).
-int split_of(long long tiles, int steps, int columns, int sms) {
-  const long long most = columns <= 64 ? 2ll * sms : sms;
-  const int least = columns <= 64 ? 1 : 4;
-  int s = 1;
-  while (s < 8 && tiles * s * 2 <= most && s * 2 * least <= steps) s *= 2;
-  return s;
+// 16.2 us).  At 128 columns a tile has 64 KB of sums to exchange, so at most one
+// CTA an SM and four steps or more each (128 x 4096 x 4096: 11.6, 9.8, 8.8 and
+// 12.8 us; 1024^3, 64 tiles of four steps: 6.4 us whole, 7.2 in two).
+template <int BN>
+int split_of(long long tiles, int steps, int sms) {
+  constexpr int kTwoAnSm = (228 * 1024) / 2 - 1024 - 256;  // shared memory of a CTA of which two fit an SM
+  const long long most = BN <= 64 ? 2ll * sms : sms;
+  const int least = BN <= 64 ? 1 : 4;
+  int best = 1;
+  for (int s = 2; s <= 8; ++s)
+    if (tiles * s <= most && s * least <= steps && (BN > 64 || Split<BN>::smem_bytes(s) <= kTwoAnSm)) best = s;
+  return best;
 }
 
 template <int DT, int BN, bool kSwap>
@@ -623,9 +631,9 @@ cudaError_t split_bn(MatmulKernelParams &q, const Mx4Operand &op, const Mx4Opera
   if (q.steps > 0 && (!make_map(&q.map_p, op, 128) || !make_map(&q.map_q, oq, BN))) return cudaErrorInvalidValue;
   q.scales_p = op.scales, q.scales_q = oq.scales;
   const long long tiles = (long long)q.tiles_p * q.tiles_q;
-  const int split = split_of(tiles, q.steps, BN, sms);
-  return launch_matmul<mx4_split_kernel<DT, BN, kSwap>>(tiles * split, kSplitThreads, Split<BN>::kSmemBytes, split, s, q,
-                                                        split);
+  const int split = split_of<BN>(tiles, q.steps, sms);
+  return launch_matmul<mx4_split_kernel<DT, BN, kSwap>>(tiles * split, Split<BN>::kThreads, Split<BN>::smem_bytes(split), split, s,
+                                                        q, split);
 }
 
 template <int DT>

@@ -647,8 +647,14 @@ cudaError_t matmul_dt(const MatmulParams &p, cudaStream_t s) {
   if (p.m <= 16) return split_bn<DT, 16, true>(q, p.b, p.a, p.sms, s);
   if (p.m <= 32) return split_bn<DT, 32, true>(q, p.b, p.a, p.sms, s);
   if (p.m <= 64) return split_bn<DT, 64, true>(q, p.b, p.a, p.sms, s);
+  // Pairs once they have a tile each; and for K above 1024 once whole tiles of
+  // 128 x 128 are more than the SMs (2048 x 2048 x 4096, 64 pair tiles: 10.7 us
+  // against 12.8; 512 x 4096 x 4096, 32: 9.9 against 9.0; 2048 x 2048 x 512: 6.2
+  // against 5.5).
   const long long pair_tiles = ceil_div(p.m, (long long)kPM) * ceil_div(p.n, (long long)kPN);
-  if (p.k == 0 || pair_tiles < p.sms / 2) return split_bn<DT, 128, false>(q, p.a, p.b, p.sms, s);
+  const long long whole_tiles = ceil_div(p.m, 128ll) * ceil_div(p.n, 128ll);
+  if (q.steps == 0 || (pair_tiles < p.sms / 2 && (whole_tiles <= p.sms || q.steps <= 4)))
+    return split_bn<DT, 128, false>(q, p.a, p.b, p.sms, s);
   const long long ra = ceil_div(p.m, (long long)kMx4TileRows), rb = ceil_div(p.n, (long long)kMx4TileRows);
   if (!make_map(&q.map_p, p.a, 128) || !make_map(&q.map_q, p.b, 128) ||
       !make_scale_map(&q.map_sp, p.a.scales, ra * q.steps) || !make_scale_map(&q.map_sq, p.b.scales, rb * q.steps))

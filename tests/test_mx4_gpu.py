@@ -83,11 +83,11 @@ def test_quantize_bits(rr, rows, cols, dtype, rounding):
     assert by_rows.shape == (rows, cols) and by_cols.shape == (cols, rows)
 
 
-@pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("offset,pad", [(0, 0), (1, 3), (8, 8), (3, 5)])
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("offset,pad", [(0, 0), (1, 3), (8, 8), (3, 5), (2, 1), (4, 12), (7, 9)])
 def test_quantize_strides_and_alignment(rr, dtype, offset, pad):
     """Rows further apart than their length, starts off the 16-byte grid."""
-    rows, cols = 70, 301
+    rows, cols = 170, 301
     slab = torch.full((offset + rows * (cols + pad) + 16,), float("nan"), dtype=dtype, device="cuda")
     view = slab[offset:offset + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
     x = values_of(rows, cols, dtype, 5)
@@ -125,7 +125,7 @@ def test_quantize_extremes(rr):
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
-@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 33), (130, 257), (40, 512)])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 33), (130, 257), (40, 512), (50, 7), (9, 16), (5, 17), (300, 47), (260, 1001)])
 def test_dequantize(rr, rows, cols, dtype):
     data, tiles, v = ref.random_matrix(rows, cols, 7)
     q = rr.Mx4(data.cuda(), tiles.cuda(), rows, cols)
@@ -234,6 +234,36 @@ def check_values(q, want):
     assert np.array_equal(ref.values(codes, scales, q.cols), ref.values(*want, q.cols), equal_nan=True)
 
 
+def test_offsets_past_32_bits(rr):
+    """More than 2^32 elements: the last rows are those of the last rows alone."""
+    rows, cols, tail = 66_048, 65_544, 128  # 4.33e9 elements; the tail starts a scale tile
+    x = torch.empty((rows, cols), dtype=BF16, device="cuda")
+    x[:-tail].zero_()
+    x[-tail:] = values_of(tail, cols, BF16, 1).cuda()
+    last = x[-tail:]
+    q = rr.mx4_quantize(x)
+    want = rr.mx4_quantize(last)
+    assert torch.equal(q.data[-tail:], want.data) and torch.equal(q.scales[-1], want.scales[0])
+    assert not q.data[:-tail].any()
+    out = rr.mx4_dequantize(q, BF16)
+    assert torch.equal(out[-tail:], rr.mx4_dequantize(want, BF16)) and not out[:-tail].any()
+    t = rr.mx4_quantize(x, transposed=True)
+    assert torch.equal(t.data[:, -tail // 2:], rr.mx4_quantize(last, transposed=True).data)
+    del t
+    y = rr.mx4_allreduce([q, q], [out, torch.empty_like(out)])[1]  # twice the values, exact
+    assert torch.equal(y[-tail:], 2 * rr.mx4_dequantize(want, BF16)) and not y[:-tail].any()
+    d = rr.Dropout(0.4, 3, 1)
+    rr.dropout(x, d, out=y)
+    whole = rr.dropout(last.reshape(-1), d._replace(first=(rows - tail) * cols)).view(tail, cols)
+    assert torch.equal(y[-tail:], whole)
+    del y, x
+    a, b = values_of(rows, 64, F32, 2).cuda(), values_of(cols, 64, F32, 3).cuda()
+    qa, qb = rr.mx4_quantize(a), rr.mx4_quantize(b)
+    rr.mx4_matmul(qa, qb, out=out, dropout=d)
+    small = rr.mx4_matmul(rr.mx4_quantize(a[-tail:].contiguous()), qb, dropout=d._replace(first=(rows - tail) * cols))
+    assert torch.equal(out[-tail:], small)
+
+
 # --------------------------------------------------------------------- product
 
 
@@ -340,7 +370,8 @@ def test_product_carries_nan_blocks(rr, m, n):
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
-@pytest.mark.parametrize("R,rows,cols", [(1, 3, 5), (2, 1, 1), (3, 7, 33), (4, 64, 64), (5, 1, 3), (8, 130, 257), (64, 9, 40)])
+@pytest.mark.parametrize("R,rows,cols", [(1, 3, 5), (2, 1, 1), (3, 7, 33), (4, 64, 64), (5, 1, 3), (8, 130, 257), (64, 9, 40),
+                                         (3, 50, 7), (5, 33, 17), (7, 40, 48), (4, 100, 31), (64, 3, 5), (2, 300, 1000)])
 def test_allreduce_is_the_ring_of_the_values(rr, R, rows, cols, dtype):
     """Bit for bit the ring AllReduce of the values, binary32 wire."""
     qs, vals = [], []
@@ -489,3 +520,20 @@ def test_refusals(rr):
     out = torch.empty((4, 64), device="cuda")
     with pytest.raises(rr.RingError):
         rr.mx4_allreduce([q, q], [out, out])
+
+
+def test_data_parallel_example(rr):
+    """The example's layer learns on the 4-bit wire, close to the binary32 wire."""
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "mx4_data_parallel.py")
+    spec = importlib.util.spec_from_file_location("mx4_data_parallel", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    plain = example.train(3, 256, 256, 12, False)
+    small = example.train(3, 256, 256, 12, True)
+    assert plain[0] == small[0]  # the first step's forward pass is the same
+    # the loss falls to well under half, and the 4-bit wire ends within a tenth of where it began
+    assert plain[-1] < plain[0] / 2 and small[-1] < small[0] / 2
+    assert abs(small[-1] - plain[-1]) < plain[0] / 10

@@ -18,12 +18,11 @@ __device__ __forceinline__ void copy_async16(void *smem_dst, const void *src) {
 }
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Sixteen bytes kN times, neighbouring elements of x from element `at` on, of
-// which the first `valid` exist (the rest read as zero), element by element.
+// Sixteen bytes kN times, neighbouring elements of x from q on, of which the
+// first `valid` exist (the rest read as zero), element by element.
 template <int DT, int kN>
-__device__ __forceinline__ void load_ends(const QuantParams &p, long long at, int valid, uint4 out[kN]) {
+__device__ __forceinline__ void load_ends(const uint8_t *q, int valid, uint4 out[kN]) {
   constexpr int E = 16 / Fmt<DT>::bytes;
-  const uint8_t *q = static_cast<const uint8_t *>(p.x) + at * Fmt<DT>::bytes;
 #pragma unroll
   for (int n = 0; n < kN; ++n) {
     uint32_t w[4] = {0, 0, 0, 0};
@@ -56,7 +55,7 @@ __device__ __forceinline__ void take_from(const QuantParams &p, long long at, in
 #pragma unroll
     for (int j = 0; j < kN; ++j) out[j] = funnel16(v[j], v[j + 1], sh);
   } else {
-    load_ends<DT, kN>(p, at, valid, out);
+    load_ends<DT, kN>(static_cast<const uint8_t *>(p.x) + at * Fmt<DT>::bytes, valid, out);
   }
 }
 
@@ -145,31 +144,36 @@ __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ Q
   const long long c0 = (long long)tk * kMx4TileCols + cl, r0 = (long long)tr * kMx4TileRows + rl0;
   const int valid = (int)max(0ll, min(16ll, p.cols - c0));
   const bool in_row = c0 < o.row_bytes * 2;
-  const T *src = static_cast<const T *>(p.x) + r0 * p.ld + c0;  // read only where it exists
+  const int left = (int)max(-1ll, min((long long)kMx4TileRows, p.rows - r0));  // rows from this lane's first on
+  // everything below steps from one pair of rows to the warp's next
+  const uint8_t *src = static_cast<const uint8_t *>(p.x) + (r0 * p.ld + c0) * (int)sizeof(T);  // read only where it exists
+  const long long src_step = 2 * warps * p.ld * (int)sizeof(T);
   uint8_t *dst = o.data + r0 * o.row_bytes + c0 / 2;
-  const long long left = p.rows - r0;  // rows from this lane's first on
+  const long long dst_step = 2 * warps * o.row_bytes;
+  unsigned long long group = (unsigned long long)(r0 * o.row_bytes * 2 + c0) >> 3, element = (unsigned long long)(r0 * p.cols + c0);
+  const unsigned long long group_step = (unsigned long long)dst_step / 4, element_step = 2ull * warps * p.cols;
+  uint8_t *scale = tile + (cl >> 7) * kMx4AtomBytes + ((cl >> 5) & 3);
 #pragma unroll 1
   for (int k = 0; k < kMx4TileRows; k += 2 * U * warps) {
     uint4 raw[U][N];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u, src += src_step) {
       const int dr = k + u * 2 * warps;
       if (valid == 16 && dr < left) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) raw[u][j] = ldg_stream(reinterpret_cast<const uint4 *>(src + dr * p.ld) + j);
+        for (int j = 0; j < N; ++j) raw[u][j] = ldg_stream(src + 16 * j);
       } else {
-        load_ends<DT, N>(p, (r0 + dr) * p.ld + c0, dr < left ? valid : 0, raw[u]);
+        load_ends<DT, N>(src, dr < left ? valid : 0, raw[u]);
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u, dst += dst_step, group += group_step, element += element_step) {
       const int dr = k + u * 2 * warps, rl = rl0 + dr;
       uint32_t byte = 0;
       if (dr < left + lane / 16) {  // the warp's first row exists
         if constexpr (DROP) {
-          const unsigned long long i = (unsigned long long)((r0 + dr) * p.cols + c0);
-          mask8<DT>(p.drop, i, raw[u]);
-          mask8<DT>(p.drop, i + 8, raw[u] + kRaw8<DT>);
+          mask8<DT>(p.drop, element, raw[u]);
+          mask8<DT>(p.drop, element + 8, raw[u] + kRaw8<DT>);
         }
         uint32_t m = max(max_mag8<DT>(raw[u]), max_mag8<DT>(raw[u] + kRaw8<DT>));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -177,17 +181,15 @@ __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ Q
         if constexpr (DROP) m = __float_as_uint(__fmul_rn(__uint_as_float(m), p.drop.scale));
         byte = scale_byte(m);
         const float inv = inverse_scale(byte);
-        const unsigned long long group = (unsigned long long)((r0 + dr) * o.row_bytes * 2 + c0) >> 3;
         uint2 q;
         float v[8];
         widen8<DT>(raw[u], v);
         q.x = codes8<SR, DROP>(v, byte, inv, p.drop.scale, p.gen_rows, group);
         widen8<DT>(raw[u] + kRaw8<DT>, v);
         q.y = codes8<SR, DROP>(v, byte, inv, p.drop.scale, p.gen_rows, group + 1);
-        if (dr < left && in_row) *reinterpret_cast<uint2 *>(dst + dr * o.row_bytes) = q;
+        if (dr < left && in_row) *reinterpret_cast<uint2 *>(dst) = q;
       }
-      if ((lane & 1) == 0)
-        tile[(cl >> 7) * kMx4AtomBytes + (rl & 31) * 16 + (rl >> 5) * 4 + ((cl >> 5) & 3)] = (uint8_t)byte;
+      if ((lane & 1) == 0) scale[(rl & 31) * 16 + (rl >> 5) * 4] = (uint8_t)byte;
     }
   }
   __syncthreads();
@@ -266,24 +268,28 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
     constexpr int L = W / 16;  // lanes a row, sixteen neighbours each
     constexpr int N = 2 * kRaw8<DT>;
     const Mx4Out &o = p.by_rows;
-    const int cl = lane % L * 16;
-    const long long c0 = col0 + cl;
+    constexpr int S = 32 / L;   // rows a warp takes at once
+    const int cl = lane % L * 16, rl0 = warp * 16 + lane / L;
+    const long long c0 = col0 + cl, r0 = row0 + rl0;
+    const bool in_row = c0 < o.row_bytes * 2;
+    const int left = (int)max(-16ll, min((long long)kMx4TileRows, p.rows - r0));  // rows from this lane's first on
+    uint4 *at = reinterpret_cast<uint4 *>(x + rl0 * kTileRowBytes + cl * Fmt<DT>::bytes);
+    uint8_t *dst = o.data + r0 * o.row_bytes + c0 / 2;
+    unsigned long long group = (unsigned long long)(r0 * o.row_bytes * 2 + c0) >> 3, element = (unsigned long long)(r0 * p.cols + c0);
+    uint8_t *scale = scales_r[cl >> 7] + (rl0 & 31) * 16 + (rl0 >> 5) * 4 + ((cl >> 5) & 3);
 #pragma unroll 1
-    for (int k = 0; k < 16; k += 32 / L) {
-      const int rl = warp * 16 + k + lane / L;
-      const long long r = row0 + rl;
-      if (row0 + warp * 16 + k >= p.rows) {  // none of the warp's rows exist
-        if (ROWS && (lane & 1) == 0) scales_r[cl >> 7][(rl & 31) * 16 + (rl >> 5) * 4 + ((cl >> 5) & 3)] = 0;
+    for (int k = 0; k < 16; k += S, at += S * kTileRowBytes / 16, dst += S * o.row_bytes, group += S * o.row_bytes / 4,
+             element += S * p.cols, scale += S * 16) {
+      if (k >= left + lane / L) {  // none of the warp's rows exist
+        if (ROWS && (lane & 1) == 0) *scale = 0;
         continue;
       }
       uint4 raw[N];
-      uint4 *at = reinterpret_cast<uint4 *>(x + rl * kTileRowBytes + cl * Fmt<DT>::bytes);
 #pragma unroll
       for (int j = 0; j < N; ++j) raw[j] = at[j];
       if constexpr (DROP) {
-        const unsigned long long i = (unsigned long long)(r * p.cols + c0);
-        mask8<DT>(p.drop, i, raw);
-        mask8<DT>(p.drop, i + 8, raw + kRaw8<DT>);
+        mask8<DT>(p.drop, element, raw);
+        mask8<DT>(p.drop, element + 8, raw + kRaw8<DT>);
 #pragma unroll
         for (int j = 0; j < N; ++j) at[j] = raw[j];
       }
@@ -294,15 +300,14 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
         if constexpr (DROP) m = __float_as_uint(__fmul_rn(__uint_as_float(m), dscale));
         const uint32_t byte = scale_byte(m);
         const float inv = inverse_scale(byte);
-        const long long i = r * o.row_bytes * 2 + c0;
         uint2 q;
         float v[8];
         widen8<DT>(raw, v);
-        q.x = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_rows, (unsigned long long)i >> 3);
+        q.x = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_rows, group);
         widen8<DT>(raw + kRaw8<DT>, v);
-        q.y = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_rows, ((unsigned long long)i >> 3) + 1);
-        if (r < p.rows && c0 < o.row_bytes * 2) *reinterpret_cast<uint2 *>(o.data + i / 2) = q;
-        if ((lane & 1) == 0) scales_r[cl >> 7][(rl & 31) * 16 + (rl >> 5) * 4 + ((cl >> 5) & 3)] = (uint8_t)byte;
+        q.y = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_rows, group + 1);
+        if (k < left && in_row) *reinterpret_cast<uint2 *>(dst) = q;
+        if ((lane & 1) == 0) *scale = (uint8_t)byte;
       }
     }
     if constexpr (DROP && COLS) __syncthreads();
@@ -412,8 +417,9 @@ cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
   const bool rows = p.by_rows.data, cols = p.by_cols.data;
   if (!cols && p.vec) {
     const long long grid = ceil_div(p.rows, (long long)kMx4TileRows) * p.by_rows.tiles_k;
-    // few tiles: more warps share a tile's rows (64 x 4096 is 16 tiles)
-    const int threads = grid >= 2ll * p.sms ? 128 : 512;
+    // four to sixteen warps a tile, to about 32 on an SM
+    int threads = 128;
+    while (threads < 512 && grid * threads < 32 * 32ll * p.sms) threads *= 2;
     return launch<mx4_rows_kernel<DT, SR, DROP>>(grid, threads, 0, s, p);
   }
   // rows off the 16-byte grid go through the tiles too (binary32 5003 x 1999

@@ -100,6 +100,13 @@ __device__ __forceinline__ void narrow8(const float v[8], uint4 *raw) {
 template <int DT>
 constexpr int kRaw8 = DT == kF32 ? 2 : 1;
 
+// 32 bytes from a 32-byte aligned address.
+__device__ __forceinline__ void ldg32(const void *p, uint4 &a, uint4 &b) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+
 // Eight elements from p, of which the first `valid` exist (the others read as
 // zero); vec: all eight exist and p is 16-byte aligned.
 template <int DT>

@@ -127,7 +127,7 @@ struct MatmulParams {
   unsigned int *status;
   int dtype, sms;
   bool vec;    // every 16-byte group of the rows of out and residual is aligned
-  bool vec32;  // every 32-byte group of the rows of out
+  bool vec32;  // every 32-byte group of them
 };
 
 cudaError_t launch_mx4_quantize_f32(const QuantParams &p, cudaStream_t s);

@@ -170,7 +170,7 @@ rr_status ring_mx4_matmul(const rr_mx4 *a, const rr_mx4 *b, void *out, size_t ld
   p.ld_out = (long long)ld, p.ld_res = (long long)ld_residual;
   p.dtype = dtype;
   p.vec = aligned16(out, m, ld, E) && (!residual || aligned16(residual, m, ld_residual, E));
-  p.vec32 = p.vec && aligned32(out, m, ld, E);
+  p.vec32 = aligned32(out, m, ld, E) && (!residual || aligned32(residual, m, ld_residual, E));
   const rr_status st = rr::device_info(&p.status, &p.sms);
   if (st != RR_OK) return st;
   return launched(rr::launch_mx4_matmul(p, stream));

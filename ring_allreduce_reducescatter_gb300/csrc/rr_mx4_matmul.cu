@@ -27,7 +27,7 @@ struct MatmulKernelParams {
   long long ld_out, ld_res;
   DropParams drop;
   unsigned int *status;
-  bool vec, vec32;  // 16- and 32-byte groups of the rows of out (and residual, for vec) are aligned
+  bool vec, vec32;  // 16- and 32-byte groups of the rows of out and residual are aligned
 };
 
 // Masks kN accumulators of one row, from column `col` on.
@@ -60,7 +60,15 @@ __device__ __forceinline__ void load_residual(const MatmulKernelParams &p, long 
   using T = typename Fmt<DT>::type;
   const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.residual) + row * p.ld_res + col);
 #pragma unroll
-  for (int j = 0; j < kN / 8 * kRaw8<DT>; ++j) res[j] = row < p.m ? ldg_l1(q + j) : make_uint4(0, 0, 0, 0);
+  for (int j = 0; j < kN / 8 * kRaw8<DT>; j += 2) {
+    if (row >= p.m) {
+      res[j] = res[j + 1] = make_uint4(0, 0, 0, 0);
+    } else if (p.vec32) {
+      ldg32(q + j, res[j], res[j + 1]);
+    } else {
+      res[j] = ldg_l1(q + j), res[j + 1] = ldg_l1(q + j + 1);
+    }
+  }
 }
 
 template <int DT, int kN>
@@ -430,9 +438,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    // The residual comes a chunk of columns ahead (the first before the tile is
-    // complete), so its latency hides behind the chunk being finished.
-    constexpr int kChunk = DT == kF32 ? 16 : 32;
+    // The residual comes 64 bytes a row ahead of the columns being finished, the
+    // first before the tile is complete, in whole sectors (16-byte loads of a
+    // lane's own row made 4096^3 with residual and dropout 42 us, now 36; more
+    // of it ahead takes registers and was no faster).
+    constexpr int kChunk = DT == kF32 ? 16 : 32, kAhead = 1;
     const int quarter = warp % 4, half = warp / 4;
     float *stage = reinterpret_cast<float *>(smem + kPairStages * kPairStageBytes) + warp * kStageFloats;
     unsigned i = 0;
@@ -441,8 +451,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const long long rows0 = (long long)tp * kPM + rank * 128 + quarter * 32, row = rows0 + lane;
       const long long col0 = (long long)tq * kPN + half * 128;
       const bool aligned = aligned_block<128>(p, col0);
-      uint4 res[2][kChunk / 8 * kRaw8<DT>];
-      if (p.residual && aligned) load_residual<DT, kChunk>(p, row, col0, res[0]);
+      uint4 res[kAhead][kChunk / 8 * kRaw8<DT>];
+      if (p.residual && aligned) {
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c) load_residual<DT, kChunk>(p, row, col0 + c * kChunk, res[c]);
+      }
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&acc_full, i & 1, kWaitLimitNs))) {
         if (lane == 0) atomicOr(p.status, kStatusWaitTimeout);
         break;
@@ -459,9 +472,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (aligned) {
 #pragma unroll
         for (int c = 0; c < 128 / kChunk; ++c) {
-          if (p.residual && c + 1 < 128 / kChunk)
-            load_residual<DT, kChunk>(p, row, col0 + (c + 1) * kChunk, res[(c + 1) & 1]);
-          finish_aligned<DT, kChunk>(p, row, col0 + c * kChunk, acc + c * kChunk, res[c & 1]);
+          finish_aligned<DT, kChunk>(p, row, col0 + c * kChunk, acc + c * kChunk, res[c % kAhead]);
+          if (p.residual && c + kAhead < 128 / kChunk)
+            load_residual<DT, kChunk>(p, row, col0 + (c + kAhead) * kChunk, res[c % kAhead]);
         }
       } else {
 #pragma unroll

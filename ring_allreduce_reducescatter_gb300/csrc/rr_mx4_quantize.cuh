@@ -417,9 +417,17 @@ cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
   const bool rows = p.by_rows.data, cols = p.by_cols.data;
   if (!cols && p.vec) {
     const long long grid = ceil_div(p.rows, (long long)kMx4TileRows) * p.by_rows.tiles_k;
-    // four to sixteen warps a tile, to about 32 on an SM
+    // More warps a tile where tiles are few.  To nearest: sixteen below two
+    // tiles an SM, else eight (8192 x 4096 bfloat16: 14.4 us, 16.4 with four);
+    // the kernels that call the generator hold 110 registers a thread and
+    // want about twelve warps an SM (4096 x 4096: 17.6 us with four warps a
+    // tile, 21.4 with sixteen; 1024 x 4096: 6.4 and 5.9).
     int threads = 128;
-    while (threads < 512 && grid * threads < 32 * 32ll * p.sms) threads *= 2;
+    if constexpr (SR || DROP) {
+      while (threads < 512 && grid * threads < 12 * 32ll * p.sms) threads *= 2;
+    } else {
+      threads = grid >= 2ll * p.sms ? 256 : 512;
+    }
     return launch<mx4_rows_kernel<DT, SR, DROP>>(grid, threads, 0, s, p);
   }
   // rows off the 16-byte grid go through the tiles too (binary32 5003 x 1999

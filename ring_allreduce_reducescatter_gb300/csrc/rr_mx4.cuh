@@ -107,6 +107,13 @@ __device__ __forceinline__ void ldg32(const void *p, uint4 &a, uint4 &b) {
                : "l"(p));
 }
 
+// The same through the read-only path without an L1 allocation.
+__device__ __forceinline__ void ldg32_stream(const void *p, uint4 &a, uint4 &b) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+
 // Eight elements from p, of which the first `valid` exist (the others read as
 // zero); vec: all eight exist and p is 16-byte aligned.
 template <int DT>

@@ -83,7 +83,7 @@ struct QuantParams {
   uintptr_t x_lo, x_hi;  // the bytes of x: [x_lo, x_hi)
   int dtype, sms;
   bool stochastic;
-  bool vec;   // every 16-byte group of a row is aligned
+  bool vec, vec32;  // 16- and 32-byte groups of the rows of x are aligned
 };
 
 struct DequantParams {

@@ -122,6 +122,7 @@ rr_status ring_mx4_quantize(const void *x, size_t rows, size_t cols, size_t ld, 
   p.dtype = dtype;
   p.stochastic = rounding == RR_MX4_STOCHASTIC;
   p.vec = aligned16(x, rows, ld, E);
+  p.vec32 = aligned32(x, rows, ld, E);
   p.x_lo = sx.lo, p.x_hi = sx.hi;
   unsigned *status;
   const rr_status st = rr::device_info(&status, &p.sms);

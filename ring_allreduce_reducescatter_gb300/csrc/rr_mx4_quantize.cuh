@@ -160,8 +160,12 @@ __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ Q
     for (int u = 0; u < U; ++u, src += src_step) {
       const int dr = k + u * 2 * warps;
       if (valid == 16 && dr < left) {
+        // (whole sectors: 16-byte loads of a lane's 32 bytes fetched each twice)
 #pragma unroll
-        for (int j = 0; j < N; ++j) raw[u][j] = ldg_stream(src + 16 * j);
+        for (int j = 0; j < N; j += 2) {
+          if (p.vec32) ldg32_stream(src + 16 * j, raw[u][j], raw[u][j + 1]);
+          else raw[u][j] = ldg_l1(src + 16 * j), raw[u][j + 1] = ldg_l1(src + 16 * j + 16);
+        }
       } else {
         load_ends<DT, N>(src, dr < left ? valid : 0, raw[u]);
       }
@@ -202,32 +206,36 @@ __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ Q
 // along the columns (the result is the transpose), with or without the rows
 // --------------------------------------------------------------------------
 
-// One CTA: 128 rows by W columns (512 bytes a row), brought to shared memory
-// by asynchronous copies, three CTAs an SM, so that one's loads run under
-// another's arithmetic.  First the rows (a lane sixteen neighbours, two lanes a
-// block; dropout is applied in place here), then the columns: a lane takes the
-// 32-bit word of one column, or two, down 32 rows, a whole block in
-// registers, two blocks one after the other, 32 bytes of codes.  (Holding the
-// tile in registers instead, 32 rows a lane, spilled: 47 us for both ways of
-// 8192 x 4096 bfloat16.)
-constexpr int kTileThreads = 256;
+// One CTA: 64 rows by W columns (512 bytes a row), brought to shared memory by
+// asynchronous copies, six CTAs an SM, so that one's loads run under another's
+// arithmetic.  First the rows (a lane sixteen neighbours, two lanes a block;
+// dropout is applied in place here), then the columns: a lane takes the 32-bit
+// word of one column, or two, down 32 rows, a whole block in registers, two
+// blocks one after the other, 32 bytes of codes.  (Holding the tile in
+// registers instead, 32 rows a lane, spilled: 47 us for both ways of
+// 8192 x 4096 bfloat16, now 21.  Tiles of 128 rows leave SMs idle at the end:
+// 4096 x 4096 stochastic both ways 30 us, now 28.)
+constexpr int kTileRows = 64;
+constexpr int kTileWarps = 4;
+constexpr int kTileThreads = 32 * kTileWarps;
 constexpr int kTileRowBytes = 512;
-constexpr int kTileSmem = kMx4TileRows * kTileRowBytes;
+constexpr int kTileSmem = kTileRows * kTileRowBytes;
+static_assert(kTileRows == 16 * kTileWarps, "a warp takes 16 rows, or a fourth of the columns");
 
 template <int DT, bool SR, bool DROP, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_constant__ QuantParams p,
+__global__ void __launch_bounds__(kTileThreads, 6) mx4_tile_kernel(const __grid_constant__ QuantParams p,
                                                                   unsigned tiles_c, bool out32) {
   grid_dependency_wait();
   grid_dependents_launch();
   constexpr int E = 16 / Fmt<DT>::bytes;              // elements in 16 bytes
   constexpr int W = kTileRowBytes / Fmt<DT>::bytes;   // columns of the CTA
   constexpr int C = 4 / Fmt<DT>::bytes;               // columns in 32 bits
-  extern __shared__ __align__(16) unsigned char x[];  // [128][512]
-  __shared__ __align__(16) uint8_t scales_r[W / 128][kMx4AtomBytes];
-  __shared__ __align__(16) uint8_t scales_c[W / 128][kMx4AtomBytes];
+  extern __shared__ __align__(16) unsigned char x[];  // [64][512]
+  __shared__ __align__(16) uint8_t scales_r[W / 128][kTileRows][4];  // of the rows, 128 columns each
+  __shared__ __align__(4) uint8_t scales_c[W][2];                     // of the columns, this CTA's two blocks
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const unsigned tc = blockIdx.x % tiles_c, tr = blockIdx.x / tiles_c;
-  const long long row0 = (long long)tr * kMx4TileRows, col0 = (long long)tc * W;
+  const long long row0 = (long long)tr * kTileRows, col0 = (long long)tc * W;
   const float dscale = DROP ? p.drop.scale : 1.f;
 
   {
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
     const long long left = p.rows - row0 - warp;  // rows from this warp's first on
     if (p.vec && valid == E) {
 #pragma unroll
-      for (int k = 0; k < kMx4TileRows; k += 8) {
+      for (int k = 0; k < kTileRows; k += kTileWarps) {
         if (k < left)
           copy_async16(dst + k * kTileRowBytes, static_cast<const uint8_t *>(p.x) + (at + k * p.ld) * Fmt<DT>::bytes);
         else
@@ -247,16 +255,16 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
     } else {
       constexpr int U = 4;
 #pragma unroll 1
-      for (int k = 0; k < kMx4TileRows; k += 8 * U) {
+      for (int k = 0; k < kTileRows; k += kTileWarps * U) {
         uint4 v[U][2], out[U];
         bool around[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          around[u] = load_around<DT, 1>(p, at + (k + 8 * u) * p.ld, k + 8 * u < left ? valid : 0, v[u]);
+          around[u] = load_around<DT, 1>(p, at + (k + kTileWarps * u) * p.ld, k + kTileWarps * u < left ? valid : 0, v[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          take_from<DT, 1>(p, at + (k + 8 * u) * p.ld, k + 8 * u < left ? valid : 0, around[u], v[u], &out[u]);
-          *reinterpret_cast<uint4 *>(dst + (k + 8 * u) * kTileRowBytes) = out[u];
+          take_from<DT, 1>(p, at + (k + kTileWarps * u) * p.ld, k + kTileWarps * u < left ? valid : 0, around[u], v[u], &out[u]);
+          *reinterpret_cast<uint4 *>(dst + (k + kTileWarps * u) * kTileRowBytes) = out[u];
         }
       }
     }
@@ -272,14 +280,14 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
     const int cl = lane % L * 16, rl0 = warp * 16 + lane / L;
     const long long c0 = col0 + cl, r0 = row0 + rl0;
     const bool in_row = c0 < o.row_bytes * 2;
-    const int left = (int)max(-16ll, min((long long)kMx4TileRows, p.rows - r0));  // rows from this lane's first on
+    const int left = (int)max(-16ll, min((long long)kTileRows, p.rows - r0));  // rows from this lane's first on
     uint4 *at = reinterpret_cast<uint4 *>(x + rl0 * kTileRowBytes + cl * Fmt<DT>::bytes);
     uint8_t *dst = o.data + r0 * o.row_bytes + c0 / 2;
     unsigned long long group = (unsigned long long)(r0 * o.row_bytes * 2 + c0) >> 3, element = (unsigned long long)(r0 * p.cols + c0);
-    uint8_t *scale = scales_r[cl >> 7] + (rl0 & 31) * 16 + (rl0 >> 5) * 4 + ((cl >> 5) & 3);
+    uint8_t *scale = &scales_r[cl >> 7][rl0][(cl >> 5) & 3];
 #pragma unroll 1
     for (int k = 0; k < 16; k += S, at += S * kTileRowBytes / 16, dst += S * o.row_bytes, group += S * o.row_bytes / 4,
-             element += S * p.cols, scale += S * 16) {
+             element += S * p.cols, scale += S * 4) {
       if (k >= left + lane / L) {  // none of the warp's rows exist
         if (ROWS && (lane & 1) == 0) *scale = 0;
         continue;
@@ -315,14 +323,14 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
 
   if constexpr (COLS) {
     const Mx4Out &o = p.by_cols;
-    const int half = warp & 1, cl = (warp >> 1) * 32 * C + lane * C;  // 64 of the rows; the lane's first column
+    const int cl = warp * 32 * C + lane * C;  // the lane's first column
     uint4 codes[C][2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      const int rl = half * 64 + b * 32;
+      const int rl = b * 32;
       if (row0 + rl >= p.rows) {  // no such block
 #pragma unroll
-        for (int c = 0; c < C; ++c) scales_c[(cl + c) >> 7][((cl + c) & 31) * 16 + (((cl + c) >> 5) & 3) * 4 + half * 2 + b] = 0;
+        for (int c = 0; c < C; ++c) scales_c[cl + c][b] = 0;
         continue;
       }
       uint32_t w[32];
@@ -354,40 +362,43 @@ __global__ void __launch_bounds__(kTileThreads, 3) mx4_tile_kernel(const __grid_
           q[g] = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_cols, group + g);
         }
         codes[c][b] = make_uint4(q[0], q[1], q[2], q[3]);
-        const int cc = cl + c;
-        scales_c[cc >> 7][(cc & 31) * 16 + ((cc >> 5) & 3) * 4 + half * 2 + b] = (uint8_t)byte;
+        scales_c[cl + c][b] = (uint8_t)byte;
       }
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const long long col = col0 + cl + c, row = row0 + half * 64;
-      if (col >= p.cols || row >= p.rows) continue;
-      uint8_t *q = o.data + col * o.row_bytes + row / 2;
-      if (out32 && row + 32 < p.rows) {
+      const long long col = col0 + cl + c;
+      if (col >= p.cols || row0 >= p.rows) continue;
+      uint8_t *q = o.data + col * o.row_bytes + row0 / 2;
+      if (out32 && row0 + 32 < p.rows) {
         stg32(q, codes[c][0], codes[c][1]);
       } else {
         *reinterpret_cast<uint4 *>(q) = codes[c][0];
-        if (row + 32 < p.rows) *reinterpret_cast<uint4 *>(q + 16) = codes[c][1];
+        if (row0 + 32 < p.rows) *reinterpret_cast<uint4 *>(q + 16) = codes[c][1];
       }
     }
   }
   __syncthreads();
-  // the scales: an atom is 128 columns by this CTA's four blocks
-  for (int k = threadIdx.x; k < W / 128 * (kMx4AtomBytes / 16); k += kTileThreads) {
-    const int a = k / (kMx4AtomBytes / 16), w = k % (kMx4AtomBytes / 16);
-    if constexpr (COLS) {
-      const Mx4Out &q = p.by_cols;
-      const long long rb = (long long)tc * (W / 128) + a;  // 128 rows of the result
+  // the scales: of a column two neighbouring bytes, of a row four for every
+  // 128 columns
+  if constexpr (COLS) {
+    const Mx4Out &q = p.by_cols;
+    for (int c = threadIdx.x; c < W; c += kTileThreads) {
+      const long long rb = (col0 + c) / kMx4TileRows;
       if (rb * kMx4TileRows < p.cols)
-        reinterpret_cast<uint4 *>(q.scales + (rb * q.tiles_k + tr / 2) * kMx4TileBytes + (tr & 1) * kMx4AtomBytes)[w] =
-            reinterpret_cast<const uint4 *>(scales_c[a])[w];
+        *reinterpret_cast<uint16_t *>(q.scales + (rb * q.tiles_k + tr / 4) * kMx4TileBytes + (tr >> 1 & 1) * kMx4AtomBytes +
+                                      (c & 31) * 16 + (c >> 5 & 3) * 4 + (tr & 1) * 2) =
+            *reinterpret_cast<const uint16_t *>(scales_c[c]);
     }
-    if constexpr (ROWS) {
-      const Mx4Out &q = p.by_rows;
-      const long long atom = (long long)tc * (W / 128) + a;  // 128 columns
-      if (row0 < p.rows && atom / 2 < q.tiles_k)
-        reinterpret_cast<uint4 *>(q.scales + (tr * q.tiles_k + atom / 2) * kMx4TileBytes + (atom & 1) * kMx4AtomBytes)[w] =
-            reinterpret_cast<const uint4 *>(scales_r[a])[w];
+  }
+  if constexpr (ROWS) {
+    const Mx4Out &q = p.by_rows;
+    for (int k = threadIdx.x; k < W / 128 * kTileRows; k += kTileThreads) {
+      const int a = k / kTileRows, r = k % kTileRows, rt = (int)(tr & 1) * kTileRows + r;  // rt: of the scale tile's rows
+      const long long atom = (long long)tc * (W / 128) + a;
+      if ((row0 - (tr & 1) * kTileRows) < p.rows && atom / 2 < q.tiles_k)
+        *reinterpret_cast<uint32_t *>(q.scales + (tr / 2 * q.tiles_k + atom / 2) * kMx4TileBytes + (atom & 1) * kMx4AtomBytes +
+                                      (rt & 31) * 16 + (rt >> 5) * 4) = *reinterpret_cast<const uint32_t *>(scales_r[a][r]);
     }
   }
 }
@@ -433,9 +444,9 @@ cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
   // rows off the 16-byte grid go through the tiles too (binary32 5003 x 1999
   // along its rows: 26 us element by element a lane)
   constexpr int W = kTileRowBytes / Fmt<DT>::bytes;
-  // tiles of 128 rows, an even number of them for the columns (a scale tile of
-  // that result spans 256 rows), and columns to whole scale tiles
-  const long long tiles_r = cols ? 2 * p.by_cols.tiles_k : ceil_div(p.rows, (long long)kMx4TileRows);
+  // rows and columns to whole scale tiles of the results (256 rows for the
+  // columns' result, 128 for the rows')
+  const long long tiles_r = cols ? 4 * p.by_cols.tiles_k : 2 * ceil_div(p.rows, (long long)kMx4TileRows);
   const long long tiles_c = ceil_div(p.cols, (long long)kMx4TileCols) * (kMx4TileCols / W);
   const bool out32 = (reinterpret_cast<uintptr_t>(p.by_cols.data) | (uintptr_t)p.by_cols.row_bytes) % 32 == 0;
   const long long grid = tiles_r * tiles_c;

@@ -191,9 +191,8 @@ struct Group {
 // the group is half a block.  Otherwise its codes are shifted into place and
 // its scales are up to three: the block of its first element, the one after
 // it, and the next row's first.
-template <bool kAligned, bool kOne>
+template <bool kAligned, bool kOne, int kB>
 __device__ __forceinline__ void fold16(const Mx4ReduceParams &p, int c, const Group &g, float sum[16]) {
-  constexpr int kB = kOne ? 1 : kAligned ? 4 : 2;
   const int R = kOne ? 1 : p.R;
   const long long at = g.row * p.row_bytes + g.col / 8 * 4;
   const long long sat = scale_offset(g.row, g.col / kMx4Block, p.tiles_k);
@@ -254,14 +253,14 @@ __device__ __forceinline__ void fold16(const Mx4ReduceParams &p, int c, const Gr
   }
 }
 
-// A group that meets several chunks: each chunk's fold, an element from its own.
+// An aligned group that meets several chunks: each chunk's fold, an element from its own.
 __device__ __noinline__ void fold_chunks(const Mx4ReduceParams &p, int first, long long i0, int valid, const Group &g,
                                          float sum[16]) {
 #pragma unroll 1
   for (int c = first; c < p.R; ++c) {
     if (c > first && i0 + valid <= c * p.base) break;
     float more[16];
-    fold16<false, false>(p, c, g, more);
+    fold16<true, false, 4>(p, c, g, more);
 #pragma unroll
     for (int j = 0; j < 16; ++j) sum[j] = c == first || i0 + j >= c * p.base ? more[j] : sum[j];
   }
@@ -305,12 +304,29 @@ __global__ void __launch_bounds__(kFlatThreads, kAligned || kOne ? 4 : 3) mx4_fo
   float sum[16];
   if (kAligned || p.cols >= 16) {
     const int first = chunk(i0);
-    if (kOne || first == p.R - 1 || i0 + valid <= (first + 1) * p.base) fold16<kAligned, kOne>(p, first, g, sum);
-    else {
-      float v[16];  // (in local memory: its address is taken)
-      fold_chunks(p, first, i0, valid, g, v);
+    if constexpr (kOne) {
+      fold16<kAligned, true, 1>(p, first, g, sum);
+    } else if constexpr (kAligned) {
+      if (first == p.R - 1 || i0 + valid <= (first + 1) * p.base) {
+        fold16<true, false, 4>(p, first, g, sum);
+      } else {
+        float v[16];  // (in local memory: its address is taken)
+        fold_chunks(p, first, i0, valid, g, v);
 #pragma unroll
-      for (int j = 0; j < 16; ++j) sum[j] = v[j];
+        for (int j = 0; j < 16; ++j) sum[j] = v[j];
+      }
+    } else {
+      // one pass, but for a group over a chunk boundary (or several); here the
+      // loop was faster than the call (1001 x 1003 over eight ranks: 16 us
+      // against 19), in the aligned kernel slower (63 against 61)
+#pragma unroll 1
+      for (int c = first; c < p.R; ++c) {
+        if (c > first && i0 + valid <= c * p.base) break;
+        float more[16];
+        fold16<false, false, 2>(p, c, g, more);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum[j] = c == first || i0 + j >= c * p.base ? more[j] : sum[j];
+      }
     }
   } else {
     long long r = g.row, c = g.col;

@@ -66,11 +66,10 @@ def _lib():
     return _L
 
 
-def _check(status: int, what: str) -> None:
-    if status:
-        from . import RingError
+def _failed(status: int, what: str):
+    from . import RingError
 
-        raise RingError(status, what)
+    raise RingError(status, what)
 
 
 class Mx4:
@@ -101,16 +100,7 @@ class Mx4:
         """A matrix whose bytes are not set yet, in one allocation."""
         if rows < 0 or cols < 0:
             raise ValueError("rows and cols must not be negative")
-        self = cls.__new__(cls)
-        n = rows * (-(-cols // 32) * 16)
-        whole = torch.empty(n + -(-rows // 128) * (-(-cols // 256) * 1024), dtype=torch.uint8,
-                            device="cuda" if device is None else device)
-        at = whole.data_ptr()
-        self.rows, self.cols, self.device = rows, cols, whole.device
-        self._data, self._scales, self._whole = None, n, whole
-        self._c = _Matrix(at, at + n, rows, cols)
-        self._at = ctypes.addressof(self._c)
-        return self
+        return _new(rows, cols, "cuda" if device is None else device)
 
     @property
     def data(self) -> torch.Tensor:
@@ -136,6 +126,19 @@ class Mx4:
 
     def __repr__(self):
         return f"Mx4({self.rows} x {self.cols}, {self.device})"
+
+
+def _new(rows, cols, device) -> Mx4:
+    """Mx4.empty without its checks."""
+    q = Mx4.__new__(Mx4)
+    n = rows * ((cols + 31) // 32 * 16)
+    whole = torch.empty(n + (rows + 127) // 128 * ((cols + 255) // 256 * 1024), dtype=torch.uint8, device=device)
+    at = whole.data_ptr()
+    q.rows, q.cols, q.device = rows, cols, whole.device
+    q._data, q._scales, q._whole = None, n, whole
+    q._c = c = _Matrix(at, at + n, rows, cols)
+    q._at = ctypes.addressof(c)
+    return q
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -200,16 +203,22 @@ def _quantize(x, want_rows, want_cols, rounding, seed, subsequence, dropout, out
     how = _ROUNDING.get(rounding)
     if how is None:
         raise ValueError(f"rounding {rounding!r}: 'nearest' or 'stochastic' is wanted")
-    if want_rows and out_rows is None:
-        out_rows = Mx4.empty(rows, cols, device)
-    if want_cols and out_cols is None:
-        out_cols = Mx4.empty(cols, rows, device)
     for q in (out_rows, out_cols):
         if q is not None and q.device != device:
             raise ValueError(f"out is on {q.device}, x on {device}")
-    _check(_lib().ring_mx4_quantize(x.data_ptr(), rows, cols, ld, code, None if out_rows is None else out_rows._at,
-                                    None if out_cols is None else out_cols._at, how, seed & _U64,
-                                    subsequence & _U64, _drop(dropout), handle), "ring_mx4_quantize")
+    by_rows = by_cols = None
+    if want_rows:
+        if out_rows is None:
+            out_rows = _new(rows, cols, device)
+        by_rows = out_rows._at
+    if want_cols:
+        if out_cols is None:
+            out_cols = _new(cols, rows, device)
+        by_cols = out_cols._at
+    status = (_L or _lib()).ring_mx4_quantize(x.data_ptr(), rows, cols, ld, code, by_rows, by_cols, how, seed & _U64,
+                                              subsequence & _U64, _drop(dropout), handle)
+    if status:
+        _failed(status, "ring_mx4_quantize")
     return out_rows, out_cols
 
 
@@ -246,7 +255,9 @@ def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.float32, out: Optional[tor
         out, ld = torch.empty((q.rows, q.cols), dtype=dtype, device=q.device), q.cols
     else:
         code, ld = _dtype(out.dtype), _output(out, q.rows, q.cols, q.device)
-    _check(_lib().ring_mx4_dequantize(q._at, out.data_ptr(), ld, code, handle), "ring_mx4_dequantize")
+    status = (_L or _lib()).ring_mx4_dequantize(q._at, out.data_ptr(), ld, code, handle)
+    if status:
+        _failed(status, "ring_mx4_dequantize")
     return out
 
 
@@ -281,8 +292,9 @@ def mx4_matmul(a: Mx4, b: Mx4, dtype: torch.dtype = torch.bfloat16, residual: Op
         ld_res, res = _output(residual, m, n, device, "residual"), residual.data_ptr()
         if residual.dtype != out.dtype:
             raise ValueError(f"residual: {residual.dtype}, the output is {out.dtype}")
-    _check(_lib().ring_mx4_matmul(a._at, b._at, out.data_ptr(), ld, code, res, ld_res, _drop(dropout), handle),
-           "ring_mx4_matmul")
+    status = (_L or _lib()).ring_mx4_matmul(a._at, b._at, out.data_ptr(), ld, code, res, ld_res, _drop(dropout), handle)
+    if status:
+        _failed(status, "ring_mx4_matmul")
     return out
 
 
@@ -299,14 +311,15 @@ def dropout(x: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] = N
 def _dropout(x, drop, residual, out):
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x: needs a CUDA tensor")
-    code, device, flat = _dtype(x.dtype), x.device, x.is_contiguous()
-    handle = _current(device)
+    device, flat = x.device, x.is_contiguous()
+    code, handle = _dtype(x.dtype), _current(device)
+    for t in (out, residual):
+        if t is not None:
+            if t.shape != x.shape or t.dtype != x.dtype or t.device != device:
+                raise ValueError("x, residual and out must have one shape, dtype and device")
+            flat = flat and t.is_contiguous()
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=device)
-    for t in (out,) if residual is None else (out, residual):
-        if t.shape != x.shape or t.dtype != x.dtype or t.device != device:
-            raise ValueError("x, residual and out must have one shape, dtype and device")
-        flat = flat and t.is_contiguous()
     if flat:
         rows, ld_x = 1, x.numel()
         cols = ld_out = ld_res = ld_x
@@ -314,8 +327,10 @@ def _dropout(x, drop, residual, out):
         rows, cols, ld_x = _matrix(x, "x")
         ld_out = _matrix(out, "out")[2]
         ld_res = cols if residual is None else _matrix(residual, "residual")[2]
-    _check(_lib().ring_dropout(x.data_ptr(), ld_x, None if residual is None else residual.data_ptr(), ld_res,
-                               out.data_ptr(), ld_out, rows, cols, code, _drop(drop), handle), "ring_dropout")
+    status = (_L or _lib()).ring_dropout(x.data_ptr(), ld_x, None if residual is None else residual.data_ptr(), ld_res,
+                                         out.data_ptr(), ld_out, rows, cols, code, _drop(drop), handle)
+    if status:
+        _failed(status, "ring_dropout")
     return out
 
 
@@ -345,7 +360,9 @@ def mx4_allreduce(qs: Sequence[Mx4], outs: Optional[Sequence[torch.Tensor]] = No
                 raise ValueError("outs: contiguous tensors of the matrices' shape and device and one dtype are wanted")
     mats = (_Matrix * R)(*[q._c for q in qs])
     ptrs = (ctypes.c_void_p * R)(*[t.data_ptr() for t in outs])
-    _check(_lib().ring_mx4_allreduce(mats, ptrs, R, _dtype(outs[0].dtype), handle), "ring_mx4_allreduce")
+    status = (_L or _lib()).ring_mx4_allreduce(mats, ptrs, R, _dtype(outs[0].dtype), handle)
+    if status:
+        _failed(status, "ring_mx4_allreduce")
     return outs
 
 

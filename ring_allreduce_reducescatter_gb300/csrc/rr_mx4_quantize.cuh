@@ -207,29 +207,35 @@ __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ Q
 // --------------------------------------------------------------------------
 
 // One CTA: 64 rows by W columns (512 bytes a row), brought to shared memory by
-// asynchronous copies, six CTAs an SM, so that one's loads run under another's
-// arithmetic.  First the rows (a lane sixteen neighbours, two lanes a block;
-// dropout is applied in place here), then the columns: a lane takes the 32-bit
-// word of one column, or two, down 32 rows, a whole block in registers, two
-// blocks one after the other, 32 bytes of codes.  (Holding the tile in
+// asynchronous copies, 24 warps an SM in several CTAs, so that one's loads run
+// under another's arithmetic.  First the rows (a lane sixteen neighbours, two
+// lanes a block; dropout is applied in place here), then the columns: a lane
+// takes the 32-bit word of one column, or two, down 32 rows, a whole block in
+// registers.  Four warps to nearest, each two blocks one after the other, so
+// that a lane stores 32 bytes, a whole sector (eight warps: columns of
+// 8192 x 4096 bfloat16 18.5 us instead of 14.7); eight where the generator
+// is called, whose long chains want more warps a tile (2048 x 4096 both ways
+// 16 us instead of 22).  (Holding the tile in
 // registers instead, 32 rows a lane, spilled: 47 us for both ways of
 // 8192 x 4096 bfloat16, now 21.  Tiles of 128 rows leave SMs idle at the end:
 // 4096 x 4096 stochastic both ways 30 us, now 28.)
 constexpr int kTileRows = 64;
-constexpr int kTileWarps = 4;
-constexpr int kTileThreads = 32 * kTileWarps;
 constexpr int kTileRowBytes = 512;
 constexpr int kTileSmem = kTileRows * kTileRowBytes;
-static_assert(kTileRows == 16 * kTileWarps, "a warp takes 16 rows, or a fourth of the columns");
+
+constexpr int tile_warps(bool generator) { return generator ? 8 : 4; }
 
 template <int DT, bool SR, bool DROP, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(kTileThreads, 6) mx4_tile_kernel(const __grid_constant__ QuantParams p,
+__global__ void __launch_bounds__(32 * tile_warps(SR || DROP), 24 / tile_warps(SR || DROP)) mx4_tile_kernel(const __grid_constant__ QuantParams p,
                                                                   unsigned tiles_c, bool out32) {
   grid_dependency_wait();
   grid_dependents_launch();
   constexpr int E = 16 / Fmt<DT>::bytes;              // elements in 16 bytes
   constexpr int W = kTileRowBytes / Fmt<DT>::bytes;   // columns of the CTA
   constexpr int C = 4 / Fmt<DT>::bytes;               // columns in 32 bits
+  constexpr int kWarps = SR || DROP ? 8 : 4, kThreads = 32 * kWarps;
+  constexpr int kWarpRows = kTileRows / kWarps;       // of the rows' part, a warp's rows
+  constexpr int kWarpBlocks = 8 / kWarps;             // of the columns' part, a warp's blocks of a fourth of the columns
   extern __shared__ __align__(16) unsigned char x[];  // [64][512]
   __shared__ __align__(16) uint8_t scales_r[W / 128][kTileRows][4];  // of the rows, 128 columns each
   __shared__ __align__(4) uint8_t scales_c[W][2];                     // of the columns, this CTA's two blocks
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kTileThreads, 6) mx4_tile_kernel(const __grid_
     const long long left = p.rows - row0 - warp;  // rows from this warp's first on
     if (p.vec && valid == E) {
 #pragma unroll
-      for (int k = 0; k < kTileRows; k += kTileWarps) {
+      for (int k = 0; k < kTileRows; k += kWarps) {
         if (k < left)
           copy_async16(dst + k * kTileRowBytes, static_cast<const uint8_t *>(p.x) + (at + k * p.ld) * Fmt<DT>::bytes);
         else
@@ -255,16 +261,16 @@ __global__ void __launch_bounds__(kTileThreads, 6) mx4_tile_kernel(const __grid_
     } else {
       constexpr int U = 4;
 #pragma unroll 1
-      for (int k = 0; k < kTileRows; k += kTileWarps * U) {
+      for (int k = 0; k < kTileRows; k += kWarps * U) {
         uint4 v[U][2], out[U];
         bool around[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          around[u] = load_around<DT, 1>(p, at + (k + kTileWarps * u) * p.ld, k + kTileWarps * u < left ? valid : 0, v[u]);
+          around[u] = load_around<DT, 1>(p, at + (k + kWarps * u) * p.ld, k + kWarps * u < left ? valid : 0, v[u]);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          take_from<DT, 1>(p, at + (k + kTileWarps * u) * p.ld, k + kTileWarps * u < left ? valid : 0, around[u], v[u], &out[u]);
-          *reinterpret_cast<uint4 *>(dst + (k + kTileWarps * u) * kTileRowBytes) = out[u];
+          take_from<DT, 1>(p, at + (k + kWarps * u) * p.ld, k + kWarps * u < left ? valid : 0, around[u], v[u], &out[u]);
+          *reinterpret_cast<uint4 *>(dst + (k + kWarps * u) * kTileRowBytes) = out[u];
         }
       }
     }
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(kTileThreads, 6) mx4_tile_kernel(const __grid_
     constexpr int N = 2 * kRaw8<DT>;
     const Mx4Out &o = p.by_rows;
     constexpr int S = 32 / L;   // rows a warp takes at once
-    const int cl = lane % L * 16, rl0 = warp * 16 + lane / L;
+    const int cl = lane % L * 16, rl0 = warp * kWarpRows + lane / L;
     const long long c0 = col0 + cl, r0 = row0 + rl0;
     const bool in_row = c0 < o.row_bytes * 2;
     const int left = (int)max(-16ll, min((long long)kTileRows, p.rows - r0));  // rows from this lane's first on
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kTileThreads, 6) mx4_tile_kernel(const __grid_
     unsigned long long group = (unsigned long long)(r0 * o.row_bytes * 2 + c0) >> 3, element = (unsigned long long)(r0 * p.cols + c0);
     uint8_t *scale = &scales_r[cl >> 7][rl0][(cl >> 5) & 3];
 #pragma unroll 1
-    for (int k = 0; k < 16; k += S, at += S * kTileRowBytes / 16, dst += S * o.row_bytes, group += S * o.row_bytes / 4,
+    for (int k = 0; k < kWarpRows; k += S, at += S * kTileRowBytes / 16, dst += S * o.row_bytes, group += S * o.row_bytes / 4,
              element += S * p.cols, scale += S * 4) {
       if (k >= left + lane / L) {  // none of the warp's rows exist
         if (ROWS && (lane & 1) == 0) *scale = 0;
@@ -323,14 +329,15 @@ __global__ void __launch_bounds__(kTileThreads, 6) mx4_tile_kernel(const __grid_
 
   if constexpr (COLS) {
     const Mx4Out &o = p.by_cols;
-    const int cl = warp * 32 * C + lane * C;  // the lane's first column
-    uint4 codes[C][2];
+    // the lane's first column, the warp's first block
+    const int cl = warp / (kWarps / 4) * 32 * C + lane * C, b0 = warp % (kWarps / 4);
+    uint4 codes[C][kWarpBlocks];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int rl = b * 32;
+    for (int b = 0; b < kWarpBlocks; ++b) {
+      const int rl = (b0 + b) * 32;
       if (row0 + rl >= p.rows) {  // no such block
 #pragma unroll
-        for (int c = 0; c < C; ++c) scales_c[cl + c][b] = 0;
+        for (int c = 0; c < C; ++c) scales_c[cl + c][b0 + b] = 0;
         continue;
       }
       uint32_t w[32];
@@ -362,19 +369,20 @@ __global__ void __launch_bounds__(kTileThreads, 6) mx4_tile_kernel(const __grid_
           q[g] = codes8<SR, DROP>(v, byte, inv, dscale, p.gen_cols, group + g);
         }
         codes[c][b] = make_uint4(q[0], q[1], q[2], q[3]);
-        scales_c[cl + c][b] = (uint8_t)byte;
+        scales_c[cl + c][b0 + b] = (uint8_t)byte;
       }
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const long long col = col0 + cl + c;
-      if (col >= p.cols || row0 >= p.rows) continue;
-      uint8_t *q = o.data + col * o.row_bytes + row0 / 2;
-      if (out32 && row0 + 32 < p.rows) {
-        stg32(q, codes[c][0], codes[c][1]);
+      const long long row = row0 + b0 * 32;
+      if (col >= p.cols || row >= p.rows) continue;
+      uint8_t *q = o.data + col * o.row_bytes + row / 2;
+      if (kWarpBlocks == 2 && out32 && row + 32 < p.rows) {
+        stg32(q, codes[c][0], codes[c][kWarpBlocks - 1]);
       } else {
         *reinterpret_cast<uint4 *>(q) = codes[c][0];
-        if (row0 + 32 < p.rows) *reinterpret_cast<uint4 *>(q + 16) = codes[c][1];
+        if (kWarpBlocks == 2 && row + 32 < p.rows) *reinterpret_cast<uint4 *>(q + 16) = codes[c][kWarpBlocks - 1];
       }
     }
   }
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(kTileThreads, 6) mx4_tile_kernel(const __grid_
   // 128 columns
   if constexpr (COLS) {
     const Mx4Out &q = p.by_cols;
-    for (int c = threadIdx.x; c < W; c += kTileThreads) {
+    for (int c = threadIdx.x; c < W; c += kThreads) {
       const long long rb = (col0 + c) / kMx4TileRows;
       if (rb * kMx4TileRows < p.cols)
         *reinterpret_cast<uint16_t *>(q.scales + (rb * q.tiles_k + tr / 4) * kMx4TileBytes + (tr >> 1 & 1) * kMx4AtomBytes +
@@ -393,7 +401,7 @@ __global__ void __launch_bounds__(kTileThreads, 6) mx4_tile_kernel(const __grid_
   }
   if constexpr (ROWS) {
     const Mx4Out &q = p.by_rows;
-    for (int k = threadIdx.x; k < W / 128 * kTileRows; k += kTileThreads) {
+    for (int k = threadIdx.x; k < W / 128 * kTileRows; k += kThreads) {
       const int a = k / kTileRows, r = k % kTileRows, rt = (int)(tr & 1) * kTileRows + r;  // rt: of the scale tile's rows
       const long long atom = (long long)tc * (W / 128) + a;
       if ((row0 - (tr & 1) * kTileRows) < p.rows && atom / 2 < q.tiles_k)
@@ -425,14 +433,25 @@ cudaError_t launch(long long grid, int threads, int smem, cudaStream_t s, const 
 
 template <int DT, bool SR, bool DROP>
 cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
+  constexpr int W = kTileRowBytes / Fmt<DT>::bytes;
   const bool rows = p.by_rows.data, cols = p.by_cols.data;
-  if (!cols && p.vec) {
+  // tiles of 64 rows: rows and columns to whole scale tiles of the results
+  // (256 rows for the columns' result, 128 for the rows')
+  const long long tiles_r = cols ? 4 * p.by_cols.tiles_k : 2 * ceil_div(p.rows, (long long)kMx4TileRows);
+  const long long tiles_c = ceil_div(p.cols, (long long)kMx4TileCols) * (kMx4TileCols / W);
+  const long long tiles = tiles_r * tiles_c;
+  // Rows alone.  Off the 16-byte grid they go through the tiles too (binary32
+  // 5003 x 1999: 26 us element by element a lane, 19 so), and with the generator
+  // where tiles are at most an SM each, or more than four (300 x 4096 bfloat16
+  // 3.7 us, else 5.0; 4096 x 4096 16.1, else 17.7; but 1024 x 4096 6.8, else 5.3).
+  const bool tiled = !p.vec || ((SR || DROP) && (tiles <= p.sms || tiles > 4ll * p.sms));
+  if (!cols && !tiled) {
     const long long grid = ceil_div(p.rows, (long long)kMx4TileRows) * p.by_rows.tiles_k;
     // More warps a tile where tiles are few.  To nearest: sixteen below two
     // tiles an SM, else eight (8192 x 4096 bfloat16: 14.4 us, 16.4 with four);
     // the kernels that call the generator hold 110 registers a thread and
-    // want about twelve warps an SM (4096 x 4096: 17.6 us with four warps a
-    // tile, 21.4 with sixteen; 1024 x 4096: 6.4 and 5.9).
+    // want about twelve warps an SM (2048 x 4096: 9.7 us with eight warps a
+    // tile, 11.2 with sixteen, 12.0 with four).
     int threads = 128;
     if constexpr (SR || DROP) {
       while (threads < 512 && grid * threads < 12 * 32ll * p.sms) threads *= 2;
@@ -441,19 +460,12 @@ cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
     }
     return launch<mx4_rows_kernel<DT, SR, DROP>>(grid, threads, 0, s, p);
   }
-  // rows off the 16-byte grid go through the tiles too (binary32 5003 x 1999
-  // along its rows: 26 us element by element a lane)
-  constexpr int W = kTileRowBytes / Fmt<DT>::bytes;
-  // rows and columns to whole scale tiles of the results (256 rows for the
-  // columns' result, 128 for the rows')
-  const long long tiles_r = cols ? 4 * p.by_cols.tiles_k : 2 * ceil_div(p.rows, (long long)kMx4TileRows);
-  const long long tiles_c = ceil_div(p.cols, (long long)kMx4TileCols) * (kMx4TileCols / W);
+  constexpr int kThreads = 32 * tile_warps(SR || DROP);
   const bool out32 = (reinterpret_cast<uintptr_t>(p.by_cols.data) | (uintptr_t)p.by_cols.row_bytes) % 32 == 0;
-  const long long grid = tiles_r * tiles_c;
   const unsigned tc = (unsigned)tiles_c;
-  if (!cols) return launch<mx4_tile_kernel<DT, SR, DROP, true, false>>(grid, kTileThreads, kTileSmem, s, p, tc, out32);
-  if (rows) return launch<mx4_tile_kernel<DT, SR, DROP, true, true>>(grid, kTileThreads, kTileSmem, s, p, tc, out32);
-  return launch<mx4_tile_kernel<DT, SR, DROP, false, true>>(grid, kTileThreads, kTileSmem, s, p, tc, out32);
+  if (!cols) return launch<mx4_tile_kernel<DT, SR, DROP, true, false>>(tiles, kThreads, kTileSmem, s, p, tc, out32);
+  if (rows) return launch<mx4_tile_kernel<DT, SR, DROP, true, true>>(tiles, kThreads, kTileSmem, s, p, tc, out32);
+  return launch<mx4_tile_kernel<DT, SR, DROP, false, true>>(tiles, kThreads, kTileSmem, s, p, tc, out32);
 }
 
 template <int DT>

@@ -368,22 +368,33 @@ def mx4_allreduce(qs: Sequence[Mx4], outs: Optional[Sequence[torch.Tensor]] = No
 
 class _Linear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, w, residual, drop, seed, subsequence):
-        x_rows, x_cols = mx4_quantize_both(x)
-        w_rows, w_cols = mx4_quantize_both(w)
+    def forward(ctx, x, w, residual, drop, seed, subsequence, want_dx, want_dw):
+        # a transpose is kept for the product of the backward pass that reads it
+        x_rows, x_cols = mx4_quantize_both(x) if want_dw else (mx4_quantize(x), None)
+        w_rows, w_cols = mx4_quantize_both(w) if want_dx else (mx4_quantize(w), None)
         ctx.kept = x_cols, w_cols, drop, seed, subsequence
         ctx.has_residual = residual is not None
         return mx4_matmul(x_rows, w_rows, x.dtype, residual=residual, dropout=drop)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         x_cols, w_cols, drop, seed, subsequence = ctx.kept
-        if dy.stride(1) != 1 or dy.stride(0) < dy.shape[1]:
-            dy = dy.contiguous()
-        g_rows, g_cols = mx4_quantize_both(dy, "stochastic", seed, subsequence, dropout=drop)
-        dx = mx4_matmul(g_rows, w_cols, dy.dtype) if ctx.needs_input_grad[0] else None
-        dw = mx4_matmul(g_cols, x_cols, dy.dtype) if ctx.needs_input_grad[1] else None
-        return dx, dw, dy if ctx.has_residual else None, None, None, None
+        dx = dw = None
+        if x_cols is not None or w_cols is not None:
+            g = dy if dy.stride(1) == 1 and dy.stride(0) >= dy.shape[1] else dy.contiguous()
+            # (each rounding keeps its numbers whether or not the other is wanted)
+            if x_cols is None:
+                g_rows = mx4_quantize(g, False, "stochastic", seed, subsequence, drop)
+            elif w_cols is None:
+                g_cols = mx4_quantize(g, True, "stochastic", seed, subsequence + 1, drop)
+            else:
+                g_rows, g_cols = mx4_quantize_both(g, "stochastic", seed, subsequence, drop)
+            if w_cols is not None:
+                dx = mx4_matmul(g_rows, w_cols, dy.dtype)
+            if x_cols is not None:
+                dw = mx4_matmul(g_cols, x_cols, dy.dtype)
+        return dx, dw, dy if ctx.has_residual else None, None, None, None, None, None
 
 
 def mx4_linear(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -396,4 +407,5 @@ def mx4_linear(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.Tensor
     than the dropout's, every step."""
     if x.dtype != w.dtype or (residual is not None and residual.dtype != x.dtype):
         raise ValueError("x, w and residual must have one dtype")
-    return _Linear.apply(x, w, residual, drop, seed, subsequence)
+    grad = torch.is_grad_enabled()
+    return _Linear.apply(x, w, residual, drop, seed, subsequence, grad and x.requires_grad, grad and w.requires_grad)

@@ -412,6 +412,31 @@ def test_linear_gradients_match_the_formula(rr):
     assert torch.equal(rs.grad.cpu(), dy)
 
 
+def test_linear_gradients_one_at_a_time(rr):
+    """Either gradient alone, and neither, give the bits of both together."""
+    x, w, dy = values_of(70, 96, BF16, 1).cuda(), values_of(130, 96, BF16, 2).cuda(), values_of(70, 130, BF16, 3).cuda()
+    d = rr.Dropout(0.2, 9, 1)
+
+    def run(need_x, need_w):
+        xs, ws = x.clone().requires_grad_(need_x), w.clone().requires_grad_(need_w)
+        y = rr.mx4_linear(xs, ws, drop=d, seed=4, subsequence=10)
+        if need_x or need_w:
+            y.backward(dy)
+        return y.detach(), xs.grad, ws.grad
+
+    y, dx, dw = run(True, True)
+    assert torch.equal(run(True, False)[1], dx) and torch.equal(run(False, True)[2], dw)
+    assert torch.equal(run(False, False)[0], y) and run(True, False)[2] is None
+    with torch.no_grad():
+        assert torch.equal(rr.mx4_linear(x.clone().requires_grad_(), w, drop=d, seed=4, subsequence=10), y)
+    # a gradient that is one value spread over the matrix (stride zero)
+    xs = x.clone().requires_grad_()
+    rr.mx4_linear(xs, w, drop=d).sum().backward()
+    ones = x.clone().requires_grad_()
+    rr.mx4_linear(ones, w, drop=d).backward(torch.ones_like(y))
+    assert torch.equal(xs.grad, ones.grad)
+
+
 def test_linear_gradient_by_differences(rr):
     """Where every operand is a 4-bit value and every block's scale is held by a 6,
     the layer is exactly bilinear: differences along x and w equal the gradients."""

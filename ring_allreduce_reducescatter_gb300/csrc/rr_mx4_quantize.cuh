@@ -441,10 +441,11 @@ cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
   const long long tiles_c = ceil_div(p.cols, (long long)kMx4TileCols) * (kMx4TileCols / W);
   const long long tiles = tiles_r * tiles_c;
   // Rows alone.  Off the 16-byte grid they go through the tiles too (binary32
-  // 5003 x 1999: 26 us element by element a lane, 19 so), and with the generator
+  // 5003 x 1999: 26 us element by element a lane, 19 so), and up to 16 of them
+  // (1 x 4096: 1.8 us, 2.5 with a warp for every pair of 128), and with the generator
   // where tiles are at most an SM each, or more than four (300 x 4096 bfloat16
   // 3.7 us, else 5.0; 4096 x 4096 16.1, else 17.7; but 1024 x 4096 6.8, else 5.3).
-  const bool tiled = !p.vec || ((SR || DROP) && (tiles <= p.sms || tiles > 4ll * p.sms));
+  const bool tiled = !p.vec || p.rows <= 16 || ((SR || DROP) && (tiles <= p.sms || tiles > 4ll * p.sms));
   if (!cols && !tiled) {
     const long long grid = ceil_div(p.rows, (long long)kMx4TileRows) * p.by_rows.tiles_k;
     // More warps a tile where tiles are few.  To nearest: sixteen below two

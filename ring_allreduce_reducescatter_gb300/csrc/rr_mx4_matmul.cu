@@ -35,11 +35,19 @@ template <int kN>
 __device__ __forceinline__ void drop_row(const MatmulKernelParams &p, long long row, long long col, float v[kN]) {
   const unsigned long long i = p.drop.first + (unsigned long long)(row * p.n + col), g = i >> 3;
   const int sh = (int)(i & 7) * 2;
+  if (sh == 0) {  // apart, so that the calls, which do not depend on one another, run together
+    uint4 u[kN / 8];
+#pragma unroll
+    for (int h = 0; h < kN / 8; ++h) u[h] = philox(p.drop.gen, g + h);
+#pragma unroll
+    for (int h = 0; h < kN / 8; ++h) drop8(p.drop, u[h], v + 8 * h);
+    return;
+  }
   uint4 u = philox(p.drop.gen, g);
 #pragma unroll
   for (int h = 0; h < kN / 8; ++h) {
-    const uint4 next = sh == 0 && h + 1 == kN / 8 ? u : philox(p.drop.gen, g + h + 1);
-    drop8(p.drop, sh == 0 ? u : funnel16(u, next, sh), v + 8 * h);
+    const uint4 next = philox(p.drop.gen, g + h + 1);
+    drop8(p.drop, funnel16(u, next, sh), v + 8 * h);
     u = next;
   }
 }

@@ -203,30 +203,24 @@ __device__ __forceinline__ uint32_t pack8_nearest(const float v[8]) {
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
-// The same with stochastic rounding, of x with scale byte `byte` (inv = 2^-X).
-// |x| * 2^(-X - 126), rounded toward zero, puts the code in the top bits of a
-// binary32 word: exponent 1 is the code's exponent 1, and the code's subnormal
-// step falls on binary32's subnormals.  The 22 bits below are the fraction f
-// of a grid step; adding the number to their top 16 carries into the code
-// exactly when floor(f 2^16) + u >= 2^16.  Two bits further up the sum leaves
-// the code in the top byte, and byte permutations gather four codes, or four
-// signs, at a time.
-__device__ __forceinline__ uint32_t pack8_stochastic(float x[8], uint32_t byte, float inv, const uint4 &u) {
+// The same with stochastic rounding.  |v| * 2^-126, rounded toward zero, puts
+// the code in the top bits of a binary32 word: exponent 1 is the code's
+// exponent 1, and the code's subnormal step falls on binary32's subnormals.
+// The 22 bits below are the fraction f of a grid step; adding the number to
+// their top 16 carries into the code exactly when floor(f 2^16) + u >= 2^16.
+// Two bits further up the sum leaves the code in the top byte, and byte
+// permutations gather four codes, or four signs, at a time.
+__device__ __forceinline__ uint32_t pack8_stochastic(const float v[8], const uint4 &u) {
   const uint32_t n[4] = {u.x, u.y, u.z, u.w};
-  float k = __fmul_rn(inv, __uint_as_float(0x00800000u));  // 2^(-X - 126), exact up to X = 23
-  if (byte > 150u) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], inv);
-    k = __uint_as_float(0x00800000u);
-  }
   uint32_t s[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    s[j] = __float_as_uint(__fmul_rz(fabsf(x[j]), k)) * 4 + __byte_perm(n[j / 2], 0, (j & 1) ? 0x4324 : 0x4104);
+    s[j] = __float_as_uint(__fmul_rz(fabsf(v[j]), __uint_as_float(0x00800000u))) * 4 +
+           __byte_perm(n[j / 2], 0, (j & 1) ? 0x4324 : 0x4104);
   uint32_t even = __byte_perm(__byte_perm(s[0], s[2], 0x0073), __byte_perm(s[4], s[6], 0x0073), 0x5410);
   uint32_t odd = __byte_perm(__byte_perm(s[1], s[3], 0x0073), __byte_perm(s[5], s[7], 0x0073), 0x5410);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = __float_as_uint(x[j]);
+  for (int j = 0; j < 8; ++j) s[j] = __float_as_uint(v[j]);
   const uint32_t se = __byte_perm(__byte_perm(s[0], s[2], 0x0073), __byte_perm(s[4], s[6], 0x0073), 0x5410);
   const uint32_t so = __byte_perm(__byte_perm(s[1], s[3], 0x0073), __byte_perm(s[5], s[7], 0x0073), 0x5410);
   even |= (se & 0x80808080u) >> 4;

@@ -83,14 +83,13 @@ __device__ __forceinline__ uint32_t max_mag8(const uint4 *raw) {
   return DT == kF32 ? m : max(m & 0xffffu, m >> 16);
 }
 
-// Zeroes the dropped ones of eight elements.
+// Zeroes the dropped ones of eight elements, whose numbers are u.
 template <int DT>
-__device__ __forceinline__ void mask8(const DropParams &d, unsigned long long i, uint4 *raw) {
-  const uint4 u = numbers8(d.gen, d.first + i);
+__device__ __forceinline__ void mask8(const uint4 &u, uint32_t cut, uint4 *raw) {
   uint32_t *w = &raw[0].x;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const bool lo = kept(u, 2 * j, d.cut), hi = kept(u, 2 * j + 1, d.cut);
+    const bool lo = kept(u, 2 * j, cut), hi = kept(u, 2 * j + 1, cut);
     if constexpr (DT == kF32) {
       if (!lo) w[2 * j] = 0;
       if (!hi) w[2 * j + 1] = 0;
@@ -98,6 +97,20 @@ __device__ __forceinline__ void mask8(const DropParams &d, unsigned long long i,
       w[j] &= (lo ? 0xffffu : 0u) | (hi ? 0xffff0000u : 0u);
     }
   }
+}
+// Of sixteen elements, from element i of the tensor on.
+template <int DT>
+__device__ __forceinline__ void mask16(const DropParams &d, unsigned long long i, uint4 *raw) {
+  i += d.first;
+  const unsigned long long g = i >> 3;
+  const int sh = (int)(i & 7) * 2;
+  uint4 a = philox(d.gen, g), b = philox(d.gen, g + 1);
+  if (sh != 0) {
+    a = funnel16(a, b, sh);
+    b = funnel16(b, philox(d.gen, g + 2), sh);
+  }
+  mask8<DT>(a, d.cut, raw);
+  mask8<DT>(b, d.cut, raw + kRaw8<DT>);
 }
 
 // Eight elements of one block to codes.
@@ -108,14 +121,11 @@ __device__ __forceinline__ uint32_t codes8(float v[8], uint32_t byte, float inv,
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], dscale);
   }
-  uint32_t q;
-  if constexpr (SR) {
-    q = pack8_stochastic(v, byte, inv, philox(gen, group));
-  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
-    q = pack8_nearest(v);
-  }
+  for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], inv);
+  uint32_t q;
+  if constexpr (SR) q = pack8_stochastic(v, philox(gen, group));
+  else q = pack8_nearest(v);
   return byte == 255u ? 0u : q;
 }
 
@@ -176,8 +186,7 @@ __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ Q
       uint32_t byte = 0;
       if (dr < left + lane / 16) {  // the warp's first row exists
         if constexpr (DROP) {
-          mask8<DT>(p.drop, element, raw[u]);
-          mask8<DT>(p.drop, element + 8, raw[u] + kRaw8<DT>);
+          mask16<DT>(p.drop, element, raw[u]);
         }
         uint32_t m = max(max_mag8<DT>(raw[u]), max_mag8<DT>(raw[u] + kRaw8<DT>));
         m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
@@ -302,8 +311,7 @@ __global__ void __launch_bounds__(32 * tile_warps(SR || DROP), 24 / tile_warps(S
 #pragma unroll
       for (int j = 0; j < N; ++j) raw[j] = at[j];
       if constexpr (DROP) {
-        mask8<DT>(p.drop, element, raw);
-        mask8<DT>(p.drop, element + 8, raw + kRaw8<DT>);
+        mask16<DT>(p.drop, element, raw);
 #pragma unroll
         for (int j = 0; j < N; ++j) at[j] = raw[j];
       }
@@ -443,9 +451,11 @@ cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
   // Rows alone.  Off the 16-byte grid they go through the tiles too (binary32
   // 5003 x 1999: 26 us element by element a lane, 19 so), and up to 16 of them
   // (1 x 4096: 1.8 us, 2.5 with a warp for every pair of 128), and with the generator
-  // where tiles are at most an SM each, or more than four (300 x 4096 bfloat16
-  // 3.7 us, else 5.0; 4096 x 4096 16.1, else 17.7; but 1024 x 4096 6.8, else 5.3).
-  const bool tiled = !p.vec || p.rows <= 16 || ((SR || DROP) && (tiles <= p.sms || tiles > 4ll * p.sms));
+  // where tiles are at most an SM each, or of 16-bit formats more than four
+  // (300 x 4096 bfloat16 3.7 us, else 5.0; 4096 x 4096 16.1, else 17.7; but
+  // 1024 x 4096 6.8, else 5.3, and binary32 8192 x 4096 40.8, else 36.5).
+  const bool tiled = !p.vec || p.rows <= 16 ||
+                     ((SR || DROP) && (tiles <= p.sms || (DT != kF32 && tiles > 4ll * p.sms)));
   if (!cols && !tiled) {
     const long long grid = ceil_div(p.rows, (long long)kMx4TileRows) * p.by_rows.tiles_k;
     // More warps a tile where tiles are few.  To nearest: sixteen below two

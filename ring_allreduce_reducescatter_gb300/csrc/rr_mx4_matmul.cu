@@ -17,7 +17,7 @@ struct MatmulKernelParams {
   // the operands by their sides of the tensor cores' product: P gives the rows
   // of the accumulators, Q the columns
   CUtensorMap map_p, map_q;
-  CUtensorMap map_sp, map_sq;  // their scale tiles, 8 rows of 128 bytes each (pair kernel)
+  CUtensorMap map_sp, map_sq;  // their scale tiles (pair kernel)
   const uint8_t *scales_p, *scales_q;
   long long m, n;
   int steps;  // of K
@@ -494,13 +494,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     if (warp == 8) {
       const uint64_t pol = l2_evict_normal_policy();
       const bool one = elect_one();
-      const int row_tiles_q = (int)ceil_div(p.n, (long long)kMx4TileRows);
       unsigned g = 0;
       bool ok = true;
       for (long long t = pair; t < tiles && ok; t += pairs) {
         const int tp = (int)(t % p.tiles_p), tq = (int)(t / p.tiles_p);
-        // (a scale tile of A past the last row reads as zeros)
-        const int ra = tp * 2 + (int)rank, rb = tq * 2, rb1 = rb + 1 < row_tiles_q ? rb + 1 : rb;
+        // (scale tiles past the last rows read as zeros)
         for (int k = 0; k < p.steps; ++k, ++g) {
           const unsigned s = g % kPairStages;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((g / kPairStages) & 1) ^ 1, kWaitLimitNs)))) break;
@@ -510,9 +508,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
             tensor_load_pair(st, &p.map_p, k * kRowBytes, tp * kPM + (int)rank * 128, bar, pol);
             tensor_load_pair(st + kHalfBytes, &p.map_q, k * kRowBytes, tq * kPN + (int)rank * 128, bar, pol);
-            tensor_load_pair(st + 2 * kHalfBytes, &p.map_sp, 0, (ra * p.steps + k) * 8, bar, pol);
-            tensor_load_pair(st + 2 * kHalfBytes + kMx4TileBytes, &p.map_sq, 0, (rb * p.steps + k) * 8, bar, pol);
-            tensor_load_pair(st + 2 * kHalfBytes + 2 * kMx4TileBytes, &p.map_sq, 0, (rb1 * p.steps + k) * 8, bar, pol);
+            tensor_load_pair(st + 2 * kHalfBytes, &p.map_sp, 0, k, tp * 2 + (int)rank, bar, pol);
+            tensor_load_pair(st + 2 * kHalfBytes + kMx4TileBytes, &p.map_sq, 0, k, tq * 2, bar, pol);
           }
           __syncwarp();
         }
@@ -592,15 +589,17 @@ bool make_map(CUtensorMap *map, const Mx4Operand &o, int box_rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The map of an operand's scale tiles, 1024 bytes each as 8 rows of 128.
-bool make_scale_map(CUtensorMap *map, const uint8_t *scales, long long tiles) {
+// The map of an operand's scale tiles: [rows / 128][steps][1024 bytes], boxes of
+// one step of `box_tiles` row tiles.
+bool make_scale_map(CUtensorMap *map, const uint8_t *scales, long long row_tiles, int steps, int box_tiles) {
   const EncodeTiled fn = encode_tiled();
   if (!fn) return false;
-  const cuuint64_t dims[2] = {128, (cuuint64_t)tiles * 8};
-  const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {128, 8};
-  const cuuint32_t unit[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(scales), dims, strides, box, unit,
+  constexpr int kWords = kMx4TileBytes / 4;
+  const cuuint64_t dims[3] = {kWords, (cuuint64_t)steps, (cuuint64_t)row_tiles};
+  const cuuint64_t strides[2] = {kMx4TileBytes, (cuuint64_t)steps * kMx4TileBytes};
+  const cuuint32_t box[3] = {kWords, 1, (cuuint32_t)box_tiles};
+  const cuuint32_t unit[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t *>(scales), dims, strides, box, unit,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -678,7 +677,7 @@ cudaError_t matmul_dt(const MatmulParams &p, cudaStream_t s) {
     return split_bn<DT, 128, false>(q, p.a, p.b, p.sms, s);
   const long long ra = ceil_div(p.m, (long long)kMx4TileRows), rb = ceil_div(p.n, (long long)kMx4TileRows);
   if (!make_map(&q.map_p, p.a, 128) || !make_map(&q.map_q, p.b, 128) ||
-      !make_scale_map(&q.map_sp, p.a.scales, ra * q.steps) || !make_scale_map(&q.map_sq, p.b.scales, rb * q.steps))
+      !make_scale_map(&q.map_sp, p.a.scales, ra, q.steps, 1) || !make_scale_map(&q.map_sq, p.b.scales, rb, q.steps, 2))
     return cudaErrorInvalidValue;
   q.tiles_p = (int)ceil_div(p.m, (long long)kPM), q.tiles_q = (int)ceil_div(p.n, (long long)kPN);
   const long long grid = 2 * (pair_tiles < p.sms / 2 ? pair_tiles : p.sms / 2);

@@ -172,6 +172,15 @@ __device__ __forceinline__ void tensor_load_pair(void *smem_dst, const CUtensorM
       "l"(map), "r"(x), "r"(y), "r"(cluster_bar), "l"(pol)
       : "memory");
 }
+// Box of a three-dimensional map.
+__device__ __forceinline__ void tensor_load_pair(void *smem_dst, const CUtensorMap *map, int x, int y, int z,
+                                                 uint32_t cluster_bar, uint64_t pol) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(smem_dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(cluster_bar), "l"(pol)
+      : "memory");
+}
 __device__ __forceinline__ uint64_t l2_evict_normal_policy() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));

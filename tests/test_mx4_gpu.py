@@ -212,14 +212,15 @@ def test_dropout_gradient_by_differences(rr):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
-@pytest.mark.parametrize("rows,cols", [(1, 40), (65, 96), (130, 333)])
-def test_quantize_with_dropout(rr, rows, cols, dtype, rounding):
-    """Quantisation of a dropped-out matrix: the binary32 product, never rounded to storage."""
+@pytest.mark.parametrize("rows,cols,p", [(1, 40, 0.3), (65, 96, 0.3), (130, 333, 0.3), (66, 160, 0.999), (300, 512, 0.1)])
+def test_quantize_with_dropout(rr, rows, cols, p, dtype, rounding):
+    """Quantisation of a dropped-out matrix: the binary32 product, never rounded
+    to storage; at p = 0.999 most blocks and whole rows are empty."""
     x = values_of(rows, cols, dtype, 12)
-    factor, kept = ref.drop_factor(0.3, 21, 4, 9, rows, cols)
+    factor, kept = ref.drop_factor(p, 21, 4, 9, rows, cols)
     g = np.where(kept, (x.float() * torch.from_numpy(factor).float()).numpy(), 0).astype(np.float64)
     rnd = (lambda k: (1, 2 + k)) if rounding == "stochastic" else (lambda k: None)
-    how = dict(rounding=rounding, seed=1, subsequence=2, dropout=rr.Dropout(0.3, 21, 4, 9))
+    how = dict(rounding=rounding, seed=1, subsequence=2, dropout=rr.Dropout(p, 21, 4, 9))
     q, t = rr.mx4_quantize_both(x.cuda(), **how)
     check_values(q, ref.quantize(g, rnd(0)))
     check_values(t, ref.quantize(g.T, rnd(1)))
@@ -316,7 +317,7 @@ def test_product_places_every_element(rr, m, n, k, dtype):
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])
 @pytest.mark.parametrize("m,n,k,p", [(1, 40, 64, 0.0), (5, 33, 96, 0.2), (130, 129, 256, 0.1), (300, 264, 512, 0.5),
-                                     (2600, 2050, 320, 0.1), (2304, 2560, 64, 0.3)])
+                                     (2600, 2050, 320, 0.1), (2304, 2560, 64, 0.3), (40, 90, 128, 0.999)])
 def test_product_epilogue(rr, m, n, k, p, dtype):
     """residual + dropout(product): the elements of the plain product in binary32, masked and added."""
     da, sa, _ = ref.random_matrix(m, k, 1, spread=1)

@@ -18,10 +18,12 @@ struct MatmulKernelParams {
   // of the accumulators, Q the columns
   CUtensorMap map_p, map_q;
   CUtensorMap map_sp, map_sq;  // their scale tiles (pair kernel)
+  CUtensorMap map_qh, map_sqh;  // Q and its scales in half the rows a box (pair kernel, halved tiles)
   const uint8_t *scales_p, *scales_q;
   long long m, n;
   int steps;  // of K
   int tiles_p, tiles_q;
+  long long items, whole;  // pair kernel: pieces of work, of which the first are whole tiles, the rest halves
   void *out;
   const void *residual;
   long long ld_out, ld_res;
@@ -407,7 +409,8 @@ __global__ void __launch_bounds__(Split<BN>::kThreads, 2) mx4_split_kernel(const
 // it has; the pair needs 128.  The grid is one CTA per SM and loops over
 // tiles; eight warps take a finished tile from tensor memory into registers at
 // once (128 accumulators a thread) and store it while the next tile's products
-// run.
+// run.  Where the tiles left for the last turn are no more than half the pairs,
+// they are halved along the columns (4096^3, 3 turns and 28 tiles for 76 pairs).
 constexpr int kPM = 256, kPN = 256;
 constexpr int kPairStages = 5;
 constexpr int kPairStageBytes = 2 * kHalfBytes + 3 * kMx4TileBytes;  // + scales of 128 rows of A, 256 of B
@@ -416,6 +419,20 @@ constexpr int kPairThreads = 384;  // warps 0-7 epilogue, 8 copies, 9 products, 
 // registers a thread: 168 at launch (384 threads), 216 for the two warpgroups
 // of the epilogue and 72 for the third: 2 * 216 + 72 = 3 * 168
 constexpr uint32_t kPairScales = kPN;  // first tensor-memory column of the scales
+
+// Piece t of the work: a tile, or half of one (side 0 or 1 of its columns).
+struct PairItem {
+  int tp, tq, side;
+  bool whole;
+};
+__device__ __forceinline__ PairItem pair_item(const MatmulKernelParams &p, long long t) {
+  PairItem i;
+  i.whole = t < p.whole;
+  const long long u = i.whole ? t : p.whole + (t - p.whole) / 2;
+  i.side = i.whole ? 0 : (int)((t - p.whole) & 1);
+  i.tp = (int)(u % p.tiles_p), i.tq = (int)(u / p.tiles_p);
+  return i;
+}
 
 template <int DT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
@@ -440,7 +457,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tcgen05_fence_after();
   const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
   const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
-  const long long tiles = (long long)p.tiles_p * p.tiles_q;
   grid_dependency_wait();
   grid_dependents_launch();
 
@@ -454,13 +470,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int quarter = warp % 4, half = warp / 4;
     float *stage = reinterpret_cast<float *>(smem + kPairStages * kPairStageBytes) + warp * kStageFloats;
     unsigned i = 0;
-    for (long long t = pair; t < tiles; t += pairs, ++i) {
-      const int tp = (int)(t % p.tiles_p), tq = (int)(t / p.tiles_p);
-      const long long rows0 = (long long)tp * kPM + rank * 128 + quarter * 32, row = rows0 + lane;
-      const long long col0 = (long long)tq * kPN + half * 128;
+    for (long long t = pair; t < p.items; t += pairs, ++i) {
+      const PairItem w = pair_item(p, t);
+      const bool mine = w.whole || half == 0;  // a half tile is one half's warps' work
+      const long long rows0 = (long long)w.tp * kPM + rank * 128 + quarter * 32, row = rows0 + lane;
+      const long long col0 = (long long)w.tq * kPN + (w.whole ? half : w.side) * 128;
       const bool aligned = aligned_block<128>(p, col0);
       uint4 res[kAhead][kChunk / 8 * kRaw8<DT>];
-      if (p.residual && aligned) {
+      if (p.residual && aligned && mine) {
 #pragma unroll
         for (int c = 0; c < kAhead; ++c) load_residual<DT, kChunk>(p, row, col0 + c * kChunk, res[c]);
       }
@@ -477,6 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       tcgen05_fence_before();
       __syncwarp();
       if (lane == 0) cluster_arrive_remote(cluster_addr(&acc_empty, 0));
+      if (!mine) continue;
       if (aligned) {
 #pragma unroll
         for (int c = 0; c < 128 / kChunk; ++c) {
@@ -496,20 +514,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const bool one = elect_one();
       unsigned g = 0;
       bool ok = true;
-      for (long long t = pair; t < tiles && ok; t += pairs) {
-        const int tp = (int)(t % p.tiles_p), tq = (int)(t / p.tiles_p);
-        // (scale tiles past the last rows read as zeros)
+      for (long long t = pair; t < p.items && ok; t += pairs) {
+        const PairItem w = pair_item(p, t);
+        const uint32_t bytes = 2 * (w.whole ? kPairStageBytes : kHalfBytes * 3 / 2 + 2 * kMx4TileBytes);
+        const int row_a = w.tp * kPM + (int)rank * 128, row_b = w.tq * kPN + (w.whole ? (int)rank * 128 : w.side * 128 + (int)rank * 64);
         for (int k = 0; k < p.steps; ++k, ++g) {
           const unsigned s = g % kPairStages;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((g / kPairStages) & 1) ^ 1, kWaitLimitNs)))) break;
           unsigned char *st = smem + s * kPairStageBytes;
           const uint32_t bar = cluster_addr(&full[s], 0);
           if (one) {
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kPairStageBytes);
-            tensor_load_pair(st, &p.map_p, k * kRowBytes, tp * kPM + (int)rank * 128, bar, pol);
-            tensor_load_pair(st + kHalfBytes, &p.map_q, k * kRowBytes, tq * kPN + (int)rank * 128, bar, pol);
-            tensor_load_pair(st + 2 * kHalfBytes, &p.map_sp, 0, k, tp * 2 + (int)rank, bar, pol);
-            tensor_load_pair(st + 2 * kHalfBytes + kMx4TileBytes, &p.map_sq, 0, k, tq * 2, bar, pol);
+            // (rows past the last, of the operands and of the scale tiles, read as zeros)
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+            tensor_load_pair(st, &p.map_p, k * kRowBytes, row_a, bar, pol);
+            tensor_load_pair(st + kHalfBytes, w.whole ? &p.map_q : &p.map_qh, k * kRowBytes, row_b, bar, pol);
+            tensor_load_pair(st + 2 * kHalfBytes, &p.map_sp, 0, k, w.tp * 2 + (int)rank, bar, pol);
+            tensor_load_pair(st + 2 * kHalfBytes + kMx4TileBytes, w.whole ? &p.map_sq : &p.map_sqh, 0, k, w.tq * 2 + w.side, bar, pol);
           }
           __syncwarp();
         }
@@ -522,7 +542,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const bool one = elect_one();
       unsigned g = 0, i = 0;
       bool ok = true;
-      for (long long t = pair; t < tiles && ok; t += pairs, ++i) {
+      for (long long t = pair; t < p.items && ok; t += pairs, ++i) {
+        const bool whole = t < p.whole;
+        const uint32_t idesc = whole ? mx4_instr_desc(kPM, kPN, 0) : mx4_instr_desc(kPM, kPN / 2, 0);
         if (i > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty, (i - 1) & 1, kWaitLimitNs)))) break;
         tcgen05_fence_after();
         for (int k = 0; k < p.steps; ++k, ++g) {
@@ -537,11 +559,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             for (int j = 0; j < 2; ++j) {
               scale_copy<2>(sa + 4 * j, scale_desc(sc + j * kMx4AtomBytes));
               scale_copy<2>(sb + 8 * j, scale_desc(sc + kMx4TileBytes + j * kMx4AtomBytes));
-              scale_copy<2>(sb + 8 * j + 4, scale_desc(sc + 2 * kMx4TileBytes + j * kMx4AtomBytes));
+              if (whole) scale_copy<2>(sb + 8 * j + 4, scale_desc(sc + 2 * kMx4TileBytes + j * kMx4AtomBytes));
             }
 #pragma unroll
             for (int j = 0; j < kBK / 64; ++j)
-              mx4_mma<2>(tmem, operand_desc(a + 32 * j), operand_desc(b + 32 * j), mx4_instr_desc(kPM, kPN, (j & 1) * 2),
+              mx4_mma<2>(tmem, operand_desc(a + 32 * j), operand_desc(b + 32 * j), idesc | mx4_scale_at((j & 1) * 2),
                          sa + 4 * (j / 2), sb + 8 * (j / 2), k > 0 || j > 0);
             tcgen05_commit<2>(&empty[s]);
           }
@@ -680,7 +702,12 @@ cudaError_t matmul_dt(const MatmulParams &p, cudaStream_t s) {
       !make_scale_map(&q.map_sp, p.a.scales, ra, q.steps, 1) || !make_scale_map(&q.map_sq, p.b.scales, rb, q.steps, 2))
     return cudaErrorInvalidValue;
   q.tiles_p = (int)ceil_div(p.m, (long long)kPM), q.tiles_q = (int)ceil_div(p.n, (long long)kPN);
-  const long long grid = 2 * (pair_tiles < p.sms / 2 ? pair_tiles : p.sms / 2);
+  const long long pairs = p.sms / 2, last = pair_tiles % pairs;
+  q.whole = 2 * last <= pairs ? pair_tiles - last : pair_tiles;
+  q.items = q.whole + 2 * (pair_tiles - q.whole);
+  if (q.items > q.whole && (!make_map(&q.map_qh, p.b, 64) || !make_scale_map(&q.map_sqh, p.b.scales, rb, q.steps, 1)))
+    return cudaErrorInvalidValue;
+  const long long grid = 2 * (q.items < pairs ? q.items : pairs);
   return launch_matmul<mx4_pair_kernel<DT>>(grid, kPairThreads, kPairSmemBytes, 0, s, q);
 }
 

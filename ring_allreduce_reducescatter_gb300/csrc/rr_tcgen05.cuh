@@ -122,9 +122,12 @@ __device__ __forceinline__ void scale_copy(uint32_t tmem, uint64_t desc) {
 // E8M0 scales, both operands K-major): bits 4-5 / 29-30 the first scale byte
 // of B / A in each 32-bit column (0 or 2), 7-9 and 10-11 the element formats
 // (1: E2M1), 17-22 N / 8, 23 the scale format (1: E8M0), 27-28 M / 128.
+__device__ __forceinline__ constexpr uint32_t mx4_scale_at(int byte) {
+  return ((uint32_t)byte << 4) | ((uint32_t)byte << 29);
+}
 __device__ __forceinline__ constexpr uint32_t mx4_instr_desc(int M, int N, int scale_at) {
-  return ((uint32_t)scale_at << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-         ((uint32_t)(M >> 7) << 27) | ((uint32_t)scale_at << 29);
+  return mx4_scale_at(scale_at) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(M >> 7) << 27);
 }
 
 // D += A B^T over 64 elements of K (two scale blocks); accumulate false: D = A B^T.

@@ -689,13 +689,16 @@ cudaError_t matmul_dt(const MatmulParams &p, cudaStream_t s) {
   if (p.m <= 16) return split_bn<DT, 16, true>(q, p.b, p.a, p.sms, s);
   if (p.m <= 32) return split_bn<DT, 32, true>(q, p.b, p.a, p.sms, s);
   if (p.m <= 64) return split_bn<DT, 64, true>(q, p.b, p.a, p.sms, s);
-  // Pairs once they have a tile each; and for K above 1024 once whole tiles of
-  // 128 x 128 are more than the SMs (2048 x 2048 x 4096, 64 pair tiles: 10.7 us
-  // against 12.8; 512 x 4096 x 4096, 32: 9.9 against 9.0; 2048 x 2048 x 512: 6.2
-  // against 5.5).
+  // Pairs once they have a tile each; for K above 1024 once whole tiles of
+  // 128 x 128 are more than the SMs (2048 x 2048 x 4096, 64 pair tiles: 10.6 us
+  // against 13.0; 2048 x 2048 x 512: 6.2 against 5.6); and for K from 4096 once
+  // there are sixteen pair tiles, each then halved (512 x 4096 x 4096, 32: 8.3 us
+  // against 9.1; 1024^2 x 4096, 16: 7.3 against 7.5; 1024^3: 4.8 against 4.4).
   const long long pair_tiles = ceil_div(p.m, (long long)kPM) * ceil_div(p.n, (long long)kPN);
   const long long whole_tiles = ceil_div(p.m, 128ll) * ceil_div(p.n, 128ll);
-  if (q.steps == 0 || (pair_tiles < p.sms / 2 && (whole_tiles <= p.sms || q.steps <= 4)))
+  const bool by_pairs = pair_tiles >= p.sms / 2 || (q.steps > 4 && whole_tiles > p.sms) ||
+                        (q.steps >= 16 && pair_tiles >= 16);
+  if (q.steps == 0 || !by_pairs)
     return split_bn<DT, 128, false>(q, p.a, p.b, p.sms, s);
   const long long ra = ceil_div(p.m, (long long)kMx4TileRows), rb = ceil_div(p.n, (long long)kMx4TileRows);
   if (!make_map(&q.map_p, p.a, 128) || !make_map(&q.map_q, p.b, 128) ||

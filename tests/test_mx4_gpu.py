@@ -281,7 +281,7 @@ def product_bound(a, b, y, dtype):
 PRODUCTS = [(1, 1, 1), (1, 8, 32), (1, 300, 64), (2, 129, 65), (7, 16, 4096), (16, 128, 256), (17, 127, 257),
             (33, 512, 1000), (64, 130, 2000), (127, 64, 511), (128, 128, 128), (129, 200, 768), (200, 333, 1537),
             (256, 256, 512), (300, 520, 300), (513, 257, 1030),
-            (2561, 2050, 300), (1111, 5000, 1030), (130, 19_500, 65)]
+            (2561, 2050, 300), (1111, 5000, 1030), (130, 19_500, 65), (1000, 1021, 4100), (300, 2500, 4096)]
 
 
 @pytest.mark.parametrize("dtype", [F32, F16, BF16])

@@ -469,7 +469,8 @@ typedef struct {
  * ring_dropout -- out = (residual +) dropout(x); with x a gradient and no
  * residual it is dropout's own backward pass.  residual may be NULL.  Sums in
  * binary32, one rounding to storage.  out may be x or residual (same address
- * and ld); any other overlap is RR_ERR_ALIAS.
+ * and ld), or lie beside them in the rows of one array (same ld); any other
+ * overlap is RR_ERR_ALIAS.
  */
 rr_status ring_dropout(const void *x, size_t ld_x, const void *residual, size_t ld_residual, void *out, size_t ld_out,
                        size_t rows, size_t cols, rr_dtype dtype, const rr_dropout *drop, cudaStream_t stream);
@@ -497,7 +498,8 @@ rr_status ring_mx4_dequantize(const rr_mx4 *q, void *out, size_t ld, rr_dtype dt
  * b[j][k]): the product of two 4-bit matrices with equal cols, both held along
  * the summed axis, on the block-scaled tensor cores; sums in binary32, one
  * rounding to storage.  out: a->rows x b->rows.  residual and drop may be
- * NULL; residual may be out itself.  With cols of zero the sum is 0.
+ * NULL; residual may be out itself, or lie beside it in the rows of one array
+ * (same ld).  With cols of zero the sum is 0.
  */
 rr_status ring_mx4_matmul(const rr_mx4 *a, const rr_mx4 *b, void *out, size_t ld, rr_dtype dtype, const void *residual,
                           size_t ld_residual, const rr_dropout *drop, cudaStream_t stream);

@@ -33,6 +33,15 @@ bool matrix_span(const void *ptr, size_t rows, size_t cols, size_t ld, size_t E,
   if (ld < cols || ld > (SIZE_MAX / 8) / E / rows) return false;
   return span_of(ptr, ((rows - 1) * ld + cols) * E, E, s);
 }
+// Whether two strided matrices of rows x cols share an element.  Of one ld they
+// may lie beside one another in the rows of one array: the second begins `at`
+// bytes into a row of the first, past its last column, and ends in that row.
+bool share(const Span &a, size_t ld_a, const Span &b, size_t ld_b, size_t cols, size_t E) {
+  if (!a.overlaps(b)) return false;
+  if (ld_a != ld_b) return true;
+  const size_t row = ld_a * E, apart = a.lo < b.lo ? (b.lo - a.lo) % row : row - (a.lo - b.lo) % row, at = apart % row;
+  return at < cols * E || at + cols * E > row;
+}
 bool aligned16(const void *ptr, size_t rows, size_t ld, size_t E) {
   return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && (rows <= 1 || ld * E % 16 == 0);
 }
@@ -162,7 +171,7 @@ rr_status ring_mx4_matmul(const rr_mx4 *a, const rr_mx4 *b, void *out, size_t ld
   if (!mx4_spans(a, &sa) || !mx4_spans(b, &sb) || !matrix_span(out, m, n, ld, E, &so)) return RR_ERR_INVALID_ARG;
   if (residual && !matrix_span(residual, m, n, ld_residual, E, &sres)) return RR_ERR_INVALID_ARG;
   if (sa.overlaps(so) || sb.overlaps(so)) return RR_ERR_ALIAS;
-  if (sres.overlaps(so) && !(residual == out && ld_residual == ld)) return RR_ERR_ALIAS;
+  if (!(residual == out && ld_residual == ld) && share(sres, ld_residual, so, ld, n, E)) return RR_ERR_ALIAS;
   p.m = (long long)m, p.n = (long long)n, p.k = (long long)a->cols;
   const rr::Mx4Out oa = mx4_out(a), ob = mx4_out(b);
   p.a = rr::Mx4Operand{oa.data, oa.scales, oa.rows, oa.row_bytes};
@@ -189,8 +198,8 @@ rr_status ring_dropout(const void *x, size_t ld_x, const void *residual, size_t 
   if (!matrix_span(x, rows, cols, ld_x, E, &sx) || !matrix_span(out, rows, cols, ld_out, E, &so))
     return RR_ERR_INVALID_ARG;
   if (residual && !matrix_span(residual, rows, cols, ld_residual, E, &sr)) return RR_ERR_INVALID_ARG;
-  if (sx.overlaps(so) && !(x == out && ld_x == ld_out)) return RR_ERR_ALIAS;
-  if (sr.overlaps(so) && !(residual == out && ld_residual == ld_out)) return RR_ERR_ALIAS;
+  if (!(x == out && ld_x == ld_out) && share(sx, ld_x, so, ld_out, cols, E)) return RR_ERR_ALIAS;
+  if (!(residual == out && ld_residual == ld_out) && share(sr, ld_residual, so, ld_out, cols, E)) return RR_ERR_ALIAS;
   // rows that follow one another everywhere are one long row
   if (ld_x == cols && ld_out == cols && (!residual || ld_residual == cols)) cols *= rows, rows = 1;
   p.x = x, p.residual = residual, p.out = out;

@@ -144,6 +144,28 @@ def test_dropout_refusals(L):
     assert call(rows=1 << 40, cols=1 << 40) == EINVAL
 
 
+def test_columns_of_one_array_are_no_overlap(L):
+    """x or a residual beside the output in the rows of one array, before it and after it; a row that runs into
+    the other's columns, or another row pitch, is an overlap still."""
+    a, b = matrix(BASE, BASE + (1 << 20), 64, 96), matrix(BASE + (2 << 20), BASE + (3 << 20), 40, 96)
+    at = BASE + (4 << 20)
+
+    def product(out, res, ld=100, ld_res=100):
+        return L.ring_mx4_matmul(ctypes.byref(a), ctypes.byref(b), out, ld, BF16, res, ld_res, None, None)
+
+    def drops(x, out, res=None, ld=100, ldo=100):
+        return L.ring_dropout(x, ld, res, ld, out, ldo, 64, 40, BF16, drop(0.5), None)
+
+    for n in (40, 45, 60):
+        for p, q in ((at, at + 2 * n), (at + 2 * n, at), (at, at + 200 + 2 * n), (at + 600 + 2 * n, at)):
+            assert product(p, q) == ECUDA and drops(p, q) == ECUDA
+            assert drops(BASE, p, res=q) == ECUDA and drops(q, p, res=p) == ECUDA
+            assert product(p, q, ld_res=101) == EALIAS and drops(p, q, ldo=101) == EALIAS
+    for n in (39, 61, 99, 100, 101):
+        for p, q in ((at, at + 2 * n), (at + 2 * n, at), (at, at + 600 + 2 * n), (at + 600 + 2 * n, at)):
+            assert product(p, q) == EALIAS and drops(p, q) == EALIAS and drops(BASE, p, res=q) == EALIAS
+
+
 def test_allreduce_refusals(L):
     from ring_allreduce_reducescatter_gb300 import mx4
 

@@ -192,6 +192,22 @@ def test_dropout_strided_in_place_and_shapes(rr):
     assert torch.equal(view, want)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,n,gap", [(33, 45, 0), (300, 136, 0), (70, 129, 3)])
+def test_output_beside_its_input(rr, m, n, gap, dtype):
+    """dropout and the product's residual from one half of an array's columns into the other."""
+    d = rr.Dropout(0.25, 5)
+    qa, qb = (rr.mx4_quantize(values_of(r, 96, F32, 8 + r).cuda()) for r in (m, n))
+    for left in (True, False):
+        whole = values_of(m, 2 * n + gap, dtype, 4).cuda()
+        src, dst = (whole[:, :n], whole[:, n + gap:]) if left else (whole[:, n + gap:], whole[:, :n])
+        x = src.clone()
+        rr.dropout(src, d, out=dst)
+        assert torch.equal(dst, rr.dropout(x, d)) and torch.equal(src, x)
+        rr.mx4_matmul(qa, qb, residual=src, dropout=d, out=dst)
+        assert torch.equal(dst, rr.mx4_matmul(qa, qb, dtype, residual=x, dropout=d)) and torch.equal(src, x)
+
+
 def test_dropout_ignores_what_it_drops(rr):
     x = torch.full((4096,), float("nan"), device="cuda")
     y = rr.dropout(x, rr.Dropout(0.5, 1))

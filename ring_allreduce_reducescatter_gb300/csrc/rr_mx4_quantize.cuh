@@ -215,9 +215,9 @@ __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ Q
 // along the columns (the result is the transpose), with or without the rows
 // --------------------------------------------------------------------------
 
-// One CTA: 64 rows by W columns (512 bytes a row), brought to shared memory by
-// asynchronous copies, 24 warps an SM in several CTAs, so that one's loads run
-// under another's arithmetic.  First the rows (a lane sixteen neighbours, two
+// One CTA: 64 rows (16 where the rows' result alone is wanted) by W columns (512
+// bytes a row), brought to shared memory by asynchronous copies, 24 warps an SM
+// in several CTAs, so that one's loads run under another's arithmetic.  First the rows (a lane sixteen neighbours, two
 // lanes a block; dropout is applied in place here), then the columns: a lane
 // takes the 32-bit word of one column, or two, down 32 rows, a whole block in
 // registers.  Four warps to nearest, each two blocks one after the other, so
@@ -227,22 +227,25 @@ __global__ void __launch_bounds__(512) mx4_rows_kernel(const __grid_constant__ Q
 // 16 us instead of 22).  (Holding the tile in
 // registers instead, 32 rows a lane, spilled: 47 us for both ways of
 // 8192 x 4096 bfloat16, now 21.  Tiles of 128 rows leave SMs idle at the end:
-// 4096 x 4096 stochastic both ways 30 us, now 28.)
-constexpr int kTileRows = 64;
+// 4096 x 4096 stochastic both ways 30 us, now 28; of the rows alone, tiles of 64
+// and of 16 rows: stochastic 15.8 and 15.0 us, 5003 x 1999 binary32 to nearest
+// 19.2 and 14.5.)
 constexpr int kTileRowBytes = 512;
-constexpr int kTileSmem = kTileRows * kTileRowBytes;
 
-constexpr int tile_warps(bool generator) { return generator ? 8 : 4; }
+// Rows and warps of a tile.
+__host__ __device__ constexpr int tile_rows(bool cols) { return cols ? 64 : 16; }
+__host__ __device__ constexpr int tile_warps(bool generator, bool cols) { return cols ? (generator ? 8 : 4) : 2; }
 
 template <int DT, bool SR, bool DROP, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(32 * tile_warps(SR || DROP), 24 / tile_warps(SR || DROP)) mx4_tile_kernel(const __grid_constant__ QuantParams p,
+__global__ void __launch_bounds__(32 * tile_warps(SR || DROP, COLS), 24 / tile_warps(SR || DROP, COLS)) mx4_tile_kernel(const __grid_constant__ QuantParams p,
                                                                   unsigned tiles_c, bool out32) {
   grid_dependency_wait();
   grid_dependents_launch();
   constexpr int E = 16 / Fmt<DT>::bytes;              // elements in 16 bytes
   constexpr int W = kTileRowBytes / Fmt<DT>::bytes;   // columns of the CTA
   constexpr int C = 4 / Fmt<DT>::bytes;               // columns in 32 bits
-  constexpr int kWarps = SR || DROP ? 8 : 4, kThreads = 32 * kWarps;
+  constexpr int kWarps = tile_warps(SR || DROP, COLS), kThreads = 32 * kWarps;
+  constexpr int kTileRows = tile_rows(COLS), kTiles = kMx4TileRows / kTileRows;  // of a scale tile's rows
   constexpr int kWarpRows = kTileRows / kWarps;       // of the rows' part, a warp's rows
   constexpr int kWarpBlocks = 8 / kWarps;             // of the columns' part, a warp's blocks of a fourth of the columns
   extern __shared__ __align__(16) unsigned char x[];  // [64][512]
@@ -410,10 +413,10 @@ __global__ void __launch_bounds__(32 * tile_warps(SR || DROP), 24 / tile_warps(S
   if constexpr (ROWS) {
     const Mx4Out &q = p.by_rows;
     for (int k = threadIdx.x; k < W / 128 * kTileRows; k += kThreads) {
-      const int a = k / kTileRows, r = k % kTileRows, rt = (int)(tr & 1) * kTileRows + r;  // rt: of the scale tile's rows
+      const int a = k / kTileRows, r = k % kTileRows, rt = (int)(tr % kTiles) * kTileRows + r;  // rt: of the scale tile's rows
       const long long atom = (long long)tc * (W / 128) + a;
-      if ((row0 - (tr & 1) * kTileRows) < p.rows && atom / 2 < q.tiles_k)
-        *reinterpret_cast<uint32_t *>(q.scales + (tr / 2 * q.tiles_k + atom / 2) * kMx4TileBytes + (atom & 1) * kMx4AtomBytes +
+      if ((row0 - tr % kTiles * kTileRows) < p.rows && atom / 2 < q.tiles_k)
+        *reinterpret_cast<uint32_t *>(q.scales + (tr / kTiles * q.tiles_k + atom / 2) * kMx4TileBytes + (atom & 1) * kMx4AtomBytes +
                                       (rt & 31) * 16 + (rt >> 5) * 4) = *reinterpret_cast<const uint32_t *>(scales_r[a][r]);
     }
   }
@@ -443,25 +446,37 @@ template <int DT, bool SR, bool DROP>
 cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
   constexpr int W = kTileRowBytes / Fmt<DT>::bytes;
   const bool rows = p.by_rows.data, cols = p.by_cols.data;
-  // tiles of 64 rows: rows and columns to whole scale tiles of the results
-  // (256 rows for the columns' result, 128 for the rows')
-  const long long tiles_r = cols ? 4 * p.by_cols.tiles_k : 2 * ceil_div(p.rows, (long long)kMx4TileRows);
+  // rows and columns to whole scale tiles of the results (256 rows for the
+  // columns' result, 128 for the rows')
+  const long long tiles_r = cols ? 4 * p.by_cols.tiles_k : kMx4TileRows / tile_rows(false) * ceil_div(p.rows, (long long)kMx4TileRows);
   const long long tiles_c = ceil_div(p.cols, (long long)kMx4TileCols) * (kMx4TileCols / W);
   const long long tiles = tiles_r * tiles_c;
   // Rows alone.  Off the 16-byte grid they go through the tiles too (binary32
-  // 5003 x 1999: 26 us element by element a lane, 19 so), and up to 16 of them
-  // (1 x 4096: 1.8 us, 2.5 with a warp for every pair of 128), and with the generator
-  // where tiles are at most an SM each, or of 16-bit formats more than four
-  // (300 x 4096 bfloat16 3.7 us, else 5.0; 4096 x 4096 16.1, else 17.7; but
-  // 1024 x 4096 6.8, else 5.3, and binary32 8192 x 4096 40.8, else 36.5).
-  const bool tiled = !p.vec || p.rows <= 16 ||
-                     ((SR || DROP) && (tiles <= p.sms || (DT != kF32 && tiles > 4ll * p.sms)));
-  if (!cols && !tiled) {
+  // 5003 x 1999: 26 us element by element a lane, 14.5 so), and up to 16 of them
+  // (1 x 4096: 1.7 us, 2.5 with a warp for every pair of 128).  Else by the tiles
+  // an SM, figures being through the tiles and straight from memory, for 4096
+  // columns: their 24 warps an SM serve the generator better and few rows spread
+  // further, straight loads have less to do where memory is the bound.
+  //   16 bits, nearest: up to 48 (300 rows 2.3 and 2.9 us, 4096 8.8 and 9.3, 6000
+  //   11.5 and 12.3; 8192 14.8 and 14.3).  Stochastic: all (4096 rows 15.0 and
+  //   17.7, 8192 26.9 and 29.3).  With dropout: but seven or eight, which is a
+  //   second turn of warps on some schedulers (800 rows 6.2 and 7.4, 1024 10.0 and
+  //   7.3, 2048 13.2 and 13.8).
+  //   binary32, nearest: up to eight (450 rows 3.1 and 3.6, 600 4.4 and 3.6).  With
+  //   the generator: up to 96 (1400 rows 8.0 and 10.9, 6000 25.4 and 28.5, with
+  //   dropout 34.4 and 37.6; 1200 7.3 and 7.1, 8192 33.3 and 29.4).
+  const long long an_sm = ceil_div(tiles, (long long)p.sms);
+  constexpr bool kTiled = SR && !DROP && DT != kF32;
+  const bool tiled = kTiled || !p.vec || p.rows <= 16 ||
+                     (DT == kF32 ? an_sm <= (SR || DROP ? 96 : 8)
+                      : DROP     ? an_sm <= 6 || an_sm > 8
+                                 : an_sm <= 48);
+  if constexpr (!kTiled) if (!cols && !tiled) {
     const long long grid = ceil_div(p.rows, (long long)kMx4TileRows) * p.by_rows.tiles_k;
     // More warps a tile where tiles are few.  To nearest: sixteen below two
     // tiles an SM, else eight (8192 x 4096 bfloat16: 14.4 us, 16.4 with four);
     // the kernels that call the generator hold 110 registers a thread and
-    // want about twelve warps an SM (2048 x 4096: 9.7 us with eight warps a
+    // want about twelve warps an SM (stochastic 2048 x 4096: 9.7 us with eight warps a
     // tile, 11.2 with sixteen, 12.0 with four).
     int threads = 128;
     if constexpr (SR || DROP) {
@@ -471,12 +486,14 @@ cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
     }
     return launch<mx4_rows_kernel<DT, SR, DROP>>(grid, threads, 0, s, p);
   }
-  constexpr int kThreads = 32 * tile_warps(SR || DROP);
+  constexpr int kThreads = 32 * tile_warps(SR || DROP, true), kSmem = tile_rows(true) * kTileRowBytes;
   const bool out32 = (reinterpret_cast<uintptr_t>(p.by_cols.data) | (uintptr_t)p.by_cols.row_bytes) % 32 == 0;
   const unsigned tc = (unsigned)tiles_c;
-  if (!cols) return launch<mx4_tile_kernel<DT, SR, DROP, true, false>>(tiles, kThreads, kTileSmem, s, p, tc, out32);
-  if (rows) return launch<mx4_tile_kernel<DT, SR, DROP, true, true>>(tiles, kThreads, kTileSmem, s, p, tc, out32);
-  return launch<mx4_tile_kernel<DT, SR, DROP, false, true>>(tiles, kThreads, kTileSmem, s, p, tc, out32);
+  if (!cols)
+    return launch<mx4_tile_kernel<DT, SR, DROP, true, false>>(tiles, 32 * tile_warps(SR || DROP, false),
+                                                              tile_rows(false) * kTileRowBytes, s, p, tc, out32);
+  if (rows) return launch<mx4_tile_kernel<DT, SR, DROP, true, true>>(tiles, kThreads, kSmem, s, p, tc, out32);
+  return launch<mx4_tile_kernel<DT, SR, DROP, false, true>>(tiles, kThreads, kSmem, s, p, tc, out32);
 }
 
 template <int DT>

@@ -1,5 +1,6 @@
 """The 4-bit kernels at the sizes that choose each of them: the row kernel that
-quantises rows straight from memory where tiles are many.
+quantises rows straight from memory where tiles are many, and products of more
+than 64 rows whose K is split over clusters of two to eight CTAs.
 
 Sizes on and beyond each edge of the rules follow from the GPU's SM count.
 """
@@ -12,6 +13,7 @@ import mx4_reference as ref
 pytestmark = pytest.mark.gpu
 
 F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+HALF_ULP = {F32: 2.0 ** -24, F16: 2.0 ** -11, BF16: 2.0 ** -8}
 
 
 @pytest.fixture(scope="module")
@@ -122,3 +124,71 @@ def test_rows_of_many_tiles_in_fewer_warps(rr, monkeypatch):
     """Two scale tiles an SM and more: eight warps a tile instead of sixteen."""
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     check_rows(rr, monkeypatch, wide_array(128 * 2 * sms + 1, 252, 4, F32, 1), "nearest", 0.0)
+
+
+# -------------------------------------------------------------------- product
+
+# more than 64 rows and fewer than sixteen pairs' tiles: K in 2, 3, 4, 5, 6, 7
+# and 8 parts (four steps of 256 or more each)
+SPLITS = [(70, 200, 2048), (129, 333, 3100), (128, 264, 4000), (200, 130, 5200), (72, 136, 6200), (100, 264, 7200),
+          (512, 512, 8192), (513, 520, 8100)]
+
+
+def product_bound(a, b, y, dtype):
+    """Binary32 accumulation of ceil(K / 64) partial sums, each within 2^-22 of the sum of magnitudes, four more for
+    the sum inside 64 elements, one addition a part for at most eight parts (2^-24 each, below one more of those),
+    and the rounding to storage (to binary16's subnormals too)."""
+    mags = np.abs(a) @ np.abs(b).T
+    acc = 2.0 ** -22 * (-(-a.shape[1] // 64) + 5) * mags
+    return acc + HALF_ULP[dtype] * (np.abs(y) + acc) + (2.0 ** -25 if dtype == F16 else 0)
+
+
+def operands(rr, m, n, k, spread):
+    (da, sa, a), (db, sb, b) = ref.random_matrix(m, k, m + k, spread), ref.random_matrix(n, k, n + 3 * k, spread)
+    return rr.Mx4(da.cuda(), sa.cuda(), m, k), rr.Mx4(db.cuda(), sb.cuda(), n, k), a, b
+
+
+@pytest.mark.parametrize("m,n,k", SPLITS)
+def test_split_product(rr, m, n, k):
+    """The product, and residual + dropout(product) out of and in place, at each alignment of the rows."""
+    qa, qb, a, b = operands(rr, m, n, k, 2)
+    y = a @ b.T
+    acc = rr.mx4_matmul(qa, qb, F32)
+    factor, kept = ref.drop_factor(0.3, 77, 1, 11, m, n)
+    kept, factor = torch.from_numpy(kept).cuda(), torch.from_numpy(factor).float().cuda()
+    dropped = torch.where(kept, acc * factor, torch.zeros((), device="cuda"))
+    d = rr.Dropout(0.3, 77, 1, 11)
+    g = torch.Generator(device="cuda").manual_seed(m)
+    for dtype in (F32, F16, BF16):
+        out = rr.mx4_matmul(qa, qb, dtype)
+        bad = np.abs(out.double().cpu().numpy() - y) > product_bound(a, b, y, dtype)
+        assert not bad.any(), f"{dtype}: {bad.sum()} of {bad.size} elements, first {np.argwhere(bad)[:5].tolist()}"
+        assert torch.equal(out, acc.to(dtype)) and torch.equal(out, rr.mx4_matmul(qa, qb, dtype)), "two calls differ"
+        r = (torch.randn((m, n), generator=g, device="cuda") * 64).to(dtype)
+        want = (r.float() + dropped).to(dtype)
+        group = 16 // r.element_size()
+        ld = -(-n // (4 * group)) * 4 * group
+        for at, width in ((0, ld), (0, ld + group), (group, ld + 2 * group), (1, n + 3)):  # 32, 16, 16 bytes, none
+            slab = torch.zeros((m, width), dtype=dtype, device="cuda")
+            view = slab[:, at:at + n]
+            rr.mx4_matmul(qa, qb, residual=r, dropout=d, out=view)
+            assert torch.equal(view, want) and not slab[:, :at].any() and not slab[:, at + n:].any()
+            view.copy_(r)
+            rr.mx4_matmul(qa, qb, residual=view, dropout=d, out=view)
+            assert torch.equal(view, want) and not slab[:, :at].any() and not slab[:, at + n:].any()
+
+
+@pytest.mark.parametrize("m,n,k", SPLITS)
+def test_split_product_places_every_element(rr, m, n, k):
+    """Sums of one term each: out[i, j] is exact, so a mix-up of rows, columns, parts of K or scales shows."""
+    g = np.random.default_rng(k)
+    nb = -(-k // 32)
+    codes_a = g.integers(0, 16, (m, nb * 32))
+    codes_a[:, k:] = 0
+    scales_a, scales_b = 127 + g.integers(-3, 4, (m, nb)), 127 + g.integers(-3, 4, (n, nb))
+    codes_b = np.zeros((n, nb * 32), dtype=np.int64)
+    codes_b[np.arange(n), g.integers(0, k, n)] = 2  # 1.0
+    qa, qb = (rr.Mx4(*(torch.from_numpy(t).cuda() for t in ref.pack(c, s)), c.shape[0], k)
+              for c, s in ((codes_a, scales_a), (codes_b, scales_b)))
+    y = ref.values(codes_a, scales_a, k) @ ref.values(codes_b, scales_b, k).T
+    assert np.array_equal(rr.mx4_matmul(qa, qb, F32).double().cpu().numpy(), y)

@@ -130,9 +130,14 @@ class Mx4:
 
 def _new(rows, cols, device) -> Mx4:
     """Mx4.empty without its checks."""
-    q = Mx4.__new__(Mx4)
     n = rows * ((cols + 31) // 32 * 16)
     whole = torch.empty(n + (rows + 127) // 128 * ((cols + 255) // 256 * 1024), dtype=torch.uint8, device=device)
+    return _of(whole, n, rows, cols)
+
+
+def _of(whole, n, rows, cols) -> Mx4:
+    """The matrix whose bytes are those of `whole`: n of data, then the scales."""
+    q = Mx4.__new__(Mx4)
     at = whole.data_ptr()
     q.rows, q.cols, q.device = rows, cols, whole.device
     q._data, q._scales, q._whole = None, n, whole
@@ -372,28 +377,33 @@ class _Linear(torch.autograd.Function):
         # a transpose is kept for the product of the backward pass that reads it
         x_rows, x_cols = mx4_quantize_both(x) if want_dw else (mx4_quantize(x), None)
         w_rows, w_cols = mx4_quantize_both(w) if want_dx else (mx4_quantize(w), None)
-        ctx.kept = x_cols, w_cols, drop, seed, subsequence
-        ctx.has_residual = residual is not None
+        # as saved tensors (their bytes): released with the graph, and seen by saved-tensor hooks
+        kept = [q for q in (x_cols, w_cols) if q is not None]
+        ctx.save_for_backward(*[q._whole for q in kept])
+        ctx.sizes = [(q._scales, q.rows, q.cols) for q in kept]
+        ctx.drop, ctx.seed, ctx.subsequence = drop, seed, subsequence
+        ctx.want_dx, ctx.want_dw, ctx.has_residual = want_dx, want_dw, residual is not None
         return mx4_matmul(x_rows, w_rows, x.dtype, residual=residual, dropout=drop)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        x_cols, w_cols, drop, seed, subsequence = ctx.kept
+        want_dx, want_dw, drop, seed, subsequence = ctx.want_dx, ctx.want_dw, ctx.drop, ctx.seed, ctx.subsequence
         dx = dw = None
-        if x_cols is not None or w_cols is not None:
+        if want_dx or want_dw:
+            kept = [_of(whole, *size) for whole, size in zip(ctx.saved_tensors, ctx.sizes)]
             g = dy if dy.stride(1) == 1 and dy.stride(0) >= dy.shape[1] else dy.contiguous()
             # (each rounding keeps its numbers whether or not the other is wanted)
-            if x_cols is None:
+            if not want_dw:
                 g_rows = mx4_quantize(g, False, "stochastic", seed, subsequence, drop)
-            elif w_cols is None:
+            elif not want_dx:
                 g_cols = mx4_quantize(g, True, "stochastic", seed, subsequence + 1, drop)
             else:
                 g_rows, g_cols = mx4_quantize_both(g, "stochastic", seed, subsequence, drop)
-            if w_cols is not None:
-                dx = mx4_matmul(g_rows, w_cols, dy.dtype)
-            if x_cols is not None:
-                dw = mx4_matmul(g_cols, x_cols, dy.dtype)
+            if want_dx:
+                dx = mx4_matmul(g_rows, kept[-1], dy.dtype)
+            if want_dw:
+                dw = mx4_matmul(g_cols, kept[0], dy.dtype)
         return dx, dw, dy if ctx.has_residual else None, None, None, None, None, None
 
 

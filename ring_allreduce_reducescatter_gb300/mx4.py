@@ -305,15 +305,42 @@ def mx4_matmul(a: Mx4, b: Mx4, dtype: torch.dtype = torch.bfloat16, residual: Op
 
 def dropout(x: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] = None,
             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """(residual +) dropout(x).  The backward pass is dropout(dy, drop) with the
-    same ``drop``.  Contiguous tensors of any shape, or two-dimensional views
-    with neighbouring columns."""
+    """(residual +) dropout(x), differentiable in x and residual (the backward
+    pass is dropout(dy, drop) with the same ``drop``).  Contiguous tensors of
+    any shape, or two-dimensional views with neighbouring columns.  ``out``
+    records no gradient, so with it none may be wanted of x or residual."""
     if stream is not None:
         return _on(stream, _dropout, x, drop, residual, out)
     return _dropout(x, drop, residual, out)
 
 
+def _records(*inputs) -> bool:
+    """Whether a gradient of one of the inputs is being recorded."""
+    return any(isinstance(t, torch.Tensor) and t.requires_grad for t in inputs) and torch.is_grad_enabled()
+
+
+class _Dropped(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, drop):
+        ctx.drop = drop
+        return _dropped(x, drop, residual, None)
+
+    @staticmethod
+    def backward(ctx, dy):
+        # (the mask goes by the index in row-major order, whatever dy's layout)
+        dx = _dropout(dy.contiguous(), ctx.drop, None, None) if ctx.needs_input_grad[0] else None
+        return dx, dy if ctx.needs_input_grad[1] else None, None
+
+
 def _dropout(x, drop, residual, out):
+    if _records(x, residual):
+        if out is not None:
+            raise ValueError("out: a gradient of x or residual is being recorded, and would be lost")
+        return _Dropped.apply(x, residual, drop)
+    return _dropped(x, drop, residual, out)
+
+
+def _dropped(x, drop, residual, out):
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError("x: needs a CUDA tensor")
     device, flat = x.device, x.is_contiguous()

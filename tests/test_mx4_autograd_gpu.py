@@ -1,10 +1,11 @@
-"""What the differentiable 4-bit layer keeps for its backward pass."""
+"""What the differentiable 4-bit layer and dropout keep for their backward pass,
+and which calls record a gradient."""
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
 
-BF16 = torch.bfloat16
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
 
 
 @pytest.fixture(scope="module")
@@ -94,3 +95,88 @@ def test_a_layer_of_which_only_the_residual_learns(rr):
     y.backward(dy, retain_graph=True)
     y.backward(dy)
     assert torch.equal(r.grad, 2 * dy)
+
+
+# --------------------------------------------------------------------- dropout
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("shape", [(1,), (1000,), (33, 45), (3, 5, 7), (64, 256)])
+def test_dropout_records_its_gradient(rr, shape, dtype):
+    """dx is dropout(dy) with the same mask, the residual's gradient dy itself; the values are those without."""
+    g = torch.Generator().manual_seed(1)
+    x, r, dy = (torch.randn(shape, generator=g).to(dtype).cuda() for _ in range(3))
+    d = rr.Dropout(0.3, 8, 2, 5)
+    plain, with_r = rr.dropout(x, d), rr.dropout(x, d, residual=r)
+    x.requires_grad_(), r.requires_grad_()
+    y = rr.dropout(x, d)
+    assert y.requires_grad and torch.equal(y.detach(), plain)
+    y.backward(dy)
+    assert torch.equal(x.grad, rr.dropout(dy, d))
+    x.grad = None
+    y = rr.dropout(x, d, residual=r)
+    assert torch.equal(y.detach(), with_r)
+    y.backward(dy)
+    assert torch.equal(x.grad, rr.dropout(dy, d)) and torch.equal(r.grad, dy)
+    x.grad = r.grad = None
+    rr.dropout(x.detach(), d, residual=r).backward(dy)
+    assert x.grad is None and torch.equal(r.grad, dy)
+
+
+def test_dropout_gradients_of_any_layout(rr):
+    """A strided input, and gradients that are one value spread out or come transposed."""
+    d = rr.Dropout(0.25, 5)
+    whole = draw(33, 60, 1, F32).requires_grad_()
+    y = rr.dropout(whole[:, 3:48], d)
+    y.sum().backward()
+    want = torch.zeros_like(whole)
+    want[:, 3:48] = rr.dropout(torch.ones((33, 45), device="cuda"), d)
+    assert torch.equal(whole.grad, want)
+    x, dy = draw(33, 45, 2, F32).requires_grad_(), draw(45, 33, 3, F32)
+    rr.dropout(x, d).backward(dy.t())
+    assert torch.equal(x.grad, rr.dropout(dy.t().contiguous(), d))
+
+
+def test_dropout_gradient_of_the_gradient(rr):
+    """dropout is linear in x: the gradient with respect to dy of <dx, v> is dropout(v)."""
+    d, x, v = rr.Dropout(0.25, 5), draw(9, 40, 1, F32).requires_grad_(), draw(9, 40, 2, F32)
+    dy = draw(9, 40, 3, F32).requires_grad_()
+    dx, = torch.autograd.grad(rr.dropout(x, d), x, dy, create_graph=True)
+    dx.backward(v)
+    assert torch.equal(dy.grad, rr.dropout(v, d))
+
+
+def test_dropout_inside_a_model(rr):
+    """A gradient passes through to what lies before it (whole numbers, so every sum is exact)."""
+    g = torch.Generator().manual_seed(1)
+    x, w = (torch.randint(-4, 5, s, generator=g).float().cuda() for s in ((16, 32), (32, 24)))
+    d = rr.Dropout(0.5, 3)
+    w.requires_grad_()
+    rr.dropout(x @ w, d).square().sum().backward()
+    y = rr.dropout((x @ w).detach(), d)
+    assert torch.equal(w.grad, x.t() @ rr.dropout(2 * y, d))
+
+
+def test_dropout_on_another_stream_records_its_gradient(rr):
+    side, d = torch.cuda.Stream(), rr.Dropout(0.5, 3)
+    x, dy = draw(64, 65, 1, F32).requires_grad_(), draw(64, 65, 2, F32)
+    side.wait_stream(torch.cuda.current_stream())
+    y = rr.dropout(x, d, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    y.backward(dy)
+    assert torch.equal(x.grad, rr.dropout(dy, d))
+
+
+def test_a_given_output_records_no_gradient(rr):
+    """out= is refused where a gradient would be lost, and taken where none is recorded."""
+    d = rr.Dropout(0.5, 3)
+    x, r = draw(4, 64, 1, F32), draw(4, 64, 2, F32)
+    learns = x.clone().requires_grad_()
+    for args in (dict(x=learns, out=torch.empty_like(x)), dict(x=x, residual=learns, out=torch.empty_like(x))):
+        with pytest.raises(ValueError, match="gradient"):
+            rr.dropout(drop=d, **args)
+        with torch.no_grad():
+            assert rr.dropout(drop=d, **args) is args["out"]
+    out = torch.empty_like(x)
+    rr.dropout(x, d, residual=r, out=out)
+    assert torch.equal(out, rr.dropout(x, d, residual=r)) and not out.requires_grad

@@ -278,9 +278,15 @@ def _output(out, rows, cols, device, name="out"):
 def mx4_matmul(a: Mx4, b: Mx4, dtype: torch.dtype = torch.bfloat16, residual: Optional[torch.Tensor] = None,
                dropout: Optional[Dropout] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """(residual +) dropout(a @ b.T), a.rows x b.rows; residual has the output's
-    dtype (that of ``out`` if it is given) and may be ``out`` itself."""
+    dtype (that of ``out`` if it is given) and may be ``out`` itself.
+    Differentiable in residual (4-bit matrices hold no gradient: mx4_linear is
+    the layer that has one); with ``out``, none may be wanted."""
     if stream is not None:
         return _on(stream, mx4_matmul, a, b, dtype, residual, dropout, out)
+    if residual is not None and _records(residual):
+        if out is not None:
+            raise ValueError("out: a gradient of residual is being recorded, and would be lost")
+        return _OntoResidual.apply(residual, a, b, dtype, dropout)
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
     m, n, device = a.rows, b.rows, a.device
@@ -301,6 +307,16 @@ def mx4_matmul(a: Mx4, b: Mx4, dtype: torch.dtype = torch.bfloat16, residual: Op
     if status:
         _failed(status, "ring_mx4_matmul")
     return out
+
+
+class _OntoResidual(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, residual, a, b, dtype, drop):
+        return mx4_matmul(a, b, dtype, residual, drop)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return dy, None, None, None, None
 
 
 def dropout(x: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] = None,

@@ -180,3 +180,21 @@ def test_a_given_output_records_no_gradient(rr):
     out = torch.empty_like(x)
     rr.dropout(x, d, residual=r, out=out)
     assert torch.equal(out, rr.dropout(x, d, residual=r)) and not out.requires_grad
+
+
+def test_product_passes_the_residuals_gradient_on(rr):
+    """The 4-bit operands hold no gradient; the residual's is dy."""
+    a, b = rr.mx4_quantize(draw(40, 64, 1)), rr.mx4_quantize(draw(50, 64, 2))
+    r, dy, d = draw(40, 50, 3).requires_grad_(), draw(40, 50, 4), rr.Dropout(0.2, 1)
+    want = rr.mx4_matmul(a, b, residual=r.detach(), dropout=d)
+    for stream in (None, torch.cuda.current_stream()):
+        y = rr.mx4_matmul(a, b, residual=r, dropout=d, stream=stream)
+        assert torch.equal(y.detach(), want)
+        y.backward(dy)
+        assert torch.equal(r.grad, dy)
+        r.grad = None
+    with pytest.raises(ValueError, match="gradient"):
+        rr.mx4_matmul(a, b, residual=r, out=torch.empty_like(want))
+    with torch.no_grad():
+        out = torch.empty_like(want)
+        assert rr.mx4_matmul(a, b, residual=r, dropout=d, out=out) is out and torch.equal(out, want)

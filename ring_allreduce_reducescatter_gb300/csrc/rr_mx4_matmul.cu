@@ -3,6 +3,7 @@
 // on the block-scaled tensor cores.
 #include "rr_mx4.cuh"
 #include "rr_tcgen05.cuh"
+#include "rr_turns.h"
 
 namespace rr {
 
@@ -31,6 +32,13 @@ struct MatmulKernelParams {
   unsigned int *status;
   bool vec, vec32;  // 16- and 32-byte groups of the rows of out and residual are aligned
 };
+
+// Waits, each time up to the limit, for the turns before `end` that may still be
+// in flight on these barriers of a ring of S stages.
+template <int S>
+__device__ __forceinline__ void wait_turns(uint64_t *bars, unsigned end, unsigned long long limit_ns) {
+  each_open_turn(end, S, [&](unsigned stage, unsigned parity) { mbar_wait_bounded(&bars[stage], parity, limit_ns); });
+}
 
 // Masks kN accumulators of one row, from column `col` on.
 template <int kN>
@@ -534,10 +542,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           __syncwarp();
         }
       }
-      if (!ok) {  // gave up: let the copies in flight land (a limit, not a wait on them)
-        if (one) atomicOr(p.status, kStatusWaitTimeout);
-        for (int s = 0; s < kPairStages; ++s) mbar_wait_bounded(&full[s], 0, 10000000ull);
-      }
+      if (!ok && one) atomicOr(p.status, kStatusWaitTimeout);
+      // The copies in flight land before shared memory is given back: both CTAs'
+      // count on rank 0, for whose last barrier below rank 1 waits.
+      if (rank == 0) wait_turns<kPairStages>(full, g, kWaitLimitNs);
     } else if (warp == 9 && rank == 0) {
       const bool one = elect_one();
       unsigned g = 0, i = 0;
@@ -569,9 +577,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           __syncwarp();
         }
-        if (one) tcgen05_commit<2>(&acc_full);
+        if (ok && one) tcgen05_commit<2>(&acc_full);  // a tile that was given up is not stored
       }
-      if (!ok && one) atomicOr(p.status, kStatusWaitTimeout);
+      if (!ok) {
+        if (one) atomicOr(p.status, kStatusWaitTimeout);
+        // the products issued so far end before tensor memory is given back (a
+        // turn's commit covers all before it)
+        if (g > 0) mbar_wait_bounded(&empty[(g - 1) % kPairStages], turn_parity(g - 1, kPairStages), kWaitLimitNs);
+      }
     }
   }
   __syncwarp();

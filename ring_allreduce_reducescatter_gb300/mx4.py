@@ -283,7 +283,7 @@ def mx4_matmul(a: Mx4, b: Mx4, dtype: torch.dtype = torch.bfloat16, residual: Op
     the layer that has one); with ``out``, none may be wanted."""
     if stream is not None:
         return _on(stream, mx4_matmul, a, b, dtype, residual, dropout, out)
-    if residual is not None and _records(residual):
+    if isinstance(residual, torch.Tensor) and residual.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out: a gradient of residual is being recorded, and would be lost")
         return _OntoResidual.apply(residual, a, b, dtype, dropout)
@@ -330,16 +330,11 @@ def dropout(x: torch.Tensor, drop: Dropout, residual: Optional[torch.Tensor] = N
     return _dropout(x, drop, residual, out)
 
 
-def _records(*inputs) -> bool:
-    """Whether a gradient of one of the inputs is being recorded."""
-    return any(isinstance(t, torch.Tensor) and t.requires_grad for t in inputs) and torch.is_grad_enabled()
-
-
 class _Dropped(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, residual, drop):
         ctx.drop = drop
-        return _dropped(x, drop, residual, None)
+        return _dropout(x, drop, residual, None)  # (nothing is recorded in here)
 
     @staticmethod
     def backward(ctx, dy):
@@ -349,16 +344,12 @@ class _Dropped(torch.autograd.Function):
 
 
 def _dropout(x, drop, residual, out):
-    if _records(x, residual):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("x: needs a CUDA tensor")
+    if (x.requires_grad or (residual is not None and residual.requires_grad)) and torch.is_grad_enabled():
         if out is not None:
             raise ValueError("out: a gradient of x or residual is being recorded, and would be lost")
         return _Dropped.apply(x, residual, drop)
-    return _dropped(x, drop, residual, out)
-
-
-def _dropped(x, drop, residual, out):
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise ValueError("x: needs a CUDA tensor")
     device, flat = x.device, x.is_contiguous()
     code, handle = _dtype(x.dtype), _current(device)
     for t in (out, residual):

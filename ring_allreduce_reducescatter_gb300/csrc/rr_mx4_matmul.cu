@@ -309,14 +309,13 @@ __global__ void __launch_bounds__(Split<BN>::kThreads, 2) mx4_split_kernel(const
       }
       __syncwarp();
     }
-    if (k < n_steps) {  // gave up: wait for the copies still in flight
-      if (one) {
-        atomicOr(p.status, kStatusWaitTimeout);
-        atomicExch(&failed, 1);
-      }
-      for (int q = k > L::kStages ? k - L::kStages : 0; q < k; ++q)
-        mbar_wait_bounded(&full[q % L::kStages], (q / L::kStages) & 1, kWaitLimitNs);
+    if (k < n_steps && one) {
+      atomicOr(p.status, kStatusWaitTimeout);
+      atomicExch(&failed, 1);
     }
+    // the copies in flight land before shared memory is given back, also where
+    // it is the products that give up
+    wait_turns<L::kStages>(full, k, kWaitLimitNs);
   } else if (warp == L::kEpilogue + 1) {
     const bool one = elect_one();
     int k = 0;

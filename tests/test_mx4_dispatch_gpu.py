@@ -192,3 +192,21 @@ def test_split_product_places_every_element(rr, m, n, k):
               for c, s in ((codes_a, scales_a), (codes_b, scales_b)))
     y = ref.values(codes_a, scales_a, k) @ ref.values(codes_b, scales_b, k).T
     assert np.array_equal(rr.mx4_matmul(qa, qb, F32).double().cpu().numpy(), y)
+
+
+def test_products_after_one_another(rr):
+    """Pairs, splits and whole tiles in turn, each CTA taking over the shared memory of one before it: every
+    product has the bits it has alone."""
+    sizes = [(2048, 2304, 1100), (1, 4096, 2048), (300, 2500, 4096), (70, 200, 2048), (512, 512, 8192), (33, 1000, 700)]
+    ops, want = [], []
+    for i, (m, n, k) in enumerate(sizes):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        a, b = (rr.mx4_quantize(torch.randn((r, k), generator=g, device="cuda")) for r in (m, n))
+        ops.append((a, b))
+        want.append(rr.mx4_matmul(a, b, BF16))
+        torch.cuda.synchronize()
+    for rounds in range(20):
+        got = [[rr.mx4_matmul(a, b, BF16) for a, b in ops] for _ in range(5)]
+        for outs in got:
+            for o, w in zip(outs, want):
+                assert torch.equal(o, w)

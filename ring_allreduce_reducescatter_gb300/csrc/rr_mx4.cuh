@@ -100,7 +100,7 @@ __device__ __forceinline__ void narrow8(const float v[8], uint4 *raw) {
 template <int DT>
 constexpr int kRaw8 = DT == kF32 ? 2 : 1;
 
-// 32 bytes from a 32-byte aligned address.
+// 32 bytes from a 32-byte aligned address; the kernel may write them too.
 __device__ __forceinline__ void ldg32(const void *p, uint4 &a, uint4 &b) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
@@ -114,8 +114,25 @@ __device__ __forceinline__ void ldg32_stream(const void *p, uint4 &a, uint4 &b) 
                : "l"(p));
 }
 
+// 16 bytes that the same kernel may write: an output may be its input, and the
+// read-only path is for memory that nothing writes while the kernel runs.
+__device__ __forceinline__ uint4 ld16(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// The same without an L1 allocation, for what is read once.
+__device__ __forceinline__ uint4 ld16_stream(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // Eight elements from p, of which the first `valid` exist (the others read as
-// zero); vec: all eight exist and p is 16-byte aligned.
+// zero), where the output may be written; vec: all eight exist and p is 16-byte
+// aligned.
 template <int DT>
 __device__ __forceinline__ void load8(const void *base, long long at, int valid, bool vec, float v[8]) {
   using T = typename Fmt<DT>::type;
@@ -123,7 +140,7 @@ __device__ __forceinline__ void load8(const void *base, long long at, int valid,
   if (vec && valid >= 8) {
     uint4 raw[kRaw8<DT>];
 #pragma unroll
-    for (int j = 0; j < kRaw8<DT>; ++j) raw[j] = ldg_stream(reinterpret_cast<const uint4 *>(p) + j);
+    for (int j = 0; j < kRaw8<DT>; ++j) raw[j] = ld16_stream(reinterpret_cast<const uint4 *>(p) + j);
     widen8<DT>(raw, v);
   } else {
 #pragma unroll

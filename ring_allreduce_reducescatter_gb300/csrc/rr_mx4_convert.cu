@@ -105,7 +105,8 @@ __device__ __forceinline__ void dropout8(const DropoutParams &p, unsigned long l
 
 // One long row: a thread takes U groups of eight (one counter of the generator
 // each), a block's groups apart, all loaded before the first call of the
-// generator.
+// generator.  (The output may be x or the residual: what a thread stores, it has
+// loaded itself.)
 template <int DT, bool RES, int U>
 __global__ void __launch_bounds__(kFlatThreads) dropout_flat_kernel(const __grid_constant__ DropoutParams p) {
   grid_dependency_wait();
@@ -120,8 +121,8 @@ __global__ void __launch_bounds__(kFlatThreads) dropout_flat_kernel(const __grid
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int j = 0; j < kRaw8<DT>; ++j) {
-        raw[u][j] = ldg_stream(reinterpret_cast<const uint4 *>(x + u * kFlatThreads * 8) + j);
-        if constexpr (RES) rawr[u][j] = ldg_stream(reinterpret_cast<const uint4 *>(res + u * kFlatThreads * 8) + j);
+        raw[u][j] = ld16_stream(reinterpret_cast<const uint4 *>(x + u * kFlatThreads * 8) + j);
+        if constexpr (RES) rawr[u][j] = ld16_stream(reinterpret_cast<const uint4 *>(res + u * kFlatThreads * 8) + j);
       }
     T *o = static_cast<T *>(p.out) + c0;
 #pragma unroll

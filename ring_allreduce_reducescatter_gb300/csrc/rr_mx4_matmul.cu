@@ -87,7 +87,7 @@ __device__ __forceinline__ void load_residual(const MatmulKernelParams &p, long 
     } else if (p.vec32) {
       ldg32(q + j, res[j], res[j + 1]);
     } else {
-      res[j] = ldg_l1(q + j), res[j + 1] = ldg_l1(q + j + 1);
+      res[j] = ld16(q + j), res[j + 1] = ld16(q + j + 1);
     }
   }
 }

@@ -199,8 +199,7 @@ __device__ __forceinline__ void finish1(const MatmulKernelParams &p, long long r
 // barrier later every CTA adds up the groups it received, in rank order (so
 // the result does not depend on timing), and finishes them.  Reading the
 // operands bounds these products, and a grid of whole tiles would leave most
-// SMs without a share of the memory; S is the largest split that still fits the
-// GPU at two CTAs an SM.  (Reading the other CTAs' sums instead of sending them
+// SMs without a share of the memory; split_of below says how S is chosen.  (Reading the other CTAs' sums instead of sending them
 // took a second barrier and the latency of a remote load: 33 rows by 4096 by
 // 11008 took 9.3 us.)
 // kSwap: P is B (a weight matrix, 128 rows a tile) and Q is A (the few tokens
@@ -675,11 +674,18 @@ cudaError_t launch_matmul(long long grid, int threads, int smem, int cluster, cu
 }
 
 // CTAs a tile.  Up to 64 columns: as many as fit the GPU at two an SM, each with
-// a step or more (1 x 4096 x 4096: 10.1 us whole, 7.8, 6.2 and 5.9 us at 2, 4
-// and 8; 1 x 11008 x 4096, 86 tiles: 10.8, 9.7 and, past two an SM, 12.9 and
-// 16.2 us).  At 128 columns a tile has 64 KB of sums to exchange, so at most one
-// CTA an SM and four steps or more each (128 x 4096 x 4096: 11.6, 9.8, 8.8 and
-// 12.8 us; 1024^3, 64 tiles of four steps: 6.4 us whole, 7.2 in two).
+// a step or more (33 x 4096 x 11008: 20.2 us whole, 13.0, 9.4 and 8.8 us at 2, 4
+// and 8; 1 x 11008 x 4096, 86 tiles: 8.1 us whole, 8.7, 8.4 and, past two an SM,
+// 10.5 us at 2, 3 and 4; where both 4 and 8 fit and K is short, 4 is the faster:
+// 1 x 4096 x 4096 6.2 us whole, 4.8, 4.3 and 4.9, 64 x 4096 x 4096 9.8 us, 7.9, 6.1
+// and 6.8).  At 128 columns a tile has 64 KB of sums to exchange and there is one
+// CTA an SM, so at most that many, and four steps or more each (128 x 1024 x 4096:
+// 6.8 us whole, 6.6, 5.9 and 6.7 at 2, 4 and 8; 1024^3, 64 tiles of four steps:
+// 4.4 us whole, 5.8 in two).  The rule is not the faster side everywhere: eight
+// steps are faster whole (128 x 4096 x 2048: 5.2 us, 6.0 in two; 1024 x 1024 x 2048:
+// 5.2 and 6.4), and clusters of seven or eight with one CTA an SM do not all run
+// at once (512 x 512 x 8192: 10.2 us whole, 6.9 at 4, 7.4 at 6, 13.0 at 7 and 13.6
+// at 8, which the rule takes).
 template <int BN>
 int split_of(long long tiles, int steps, int sms) {
   constexpr int kTwoAnSm = (228 * 1024) / 2 - 1024 - 256;  // shared memory of a CTA of which two fit an SM

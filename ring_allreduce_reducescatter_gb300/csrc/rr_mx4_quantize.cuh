@@ -1,10 +1,14 @@
 // rr_mx4_quantize.cuh -- quantisation to microscaled 4 bits of one storage
 // format (compiled once for each by rr_mx4_quantize_*.cu).
 //
-// Bound by memory where the rounding is to nearest: the input is read once,
-// 17/32 of a byte an element and direction written.  Stochastic rounding adds
-// a call of the generator for every eight elements and direction, and then the
-// instruction rate bounds it.
+// Bound by memory where the rounding is to nearest, on the 16-byte grid: the
+// input is read once, 17/32 of a byte an element and direction written.
+// Stochastic rounding takes twice the instructions (8192 x 4096 bfloat16 along
+// the rows: 20.9 an element for 9.5, of which the generator's, one call for every
+// eight elements and direction, are 5) and two to four times the memory's time.
+// Two thirds of the issue slots are busy then, so neither the issue rate nor
+// memory is used up: a tile waits for all its loads before it computes, and
+// every thread sets up its addresses for 64 elements.
 #pragma once
 
 #include "rr_mx4.cuh"
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(32 * tile_warps(SR || DROP, COLS), 24 / tile_w
   constexpr int kTileRows = tile_rows(COLS), kTiles = kMx4TileRows / kTileRows;  // of a scale tile's rows
   constexpr int kWarpRows = kTileRows / kWarps;       // of the rows' part, a warp's rows
   constexpr int kWarpBlocks = 8 / kWarps;             // of the columns' part, a warp's blocks of a fourth of the columns
-  extern __shared__ __align__(16) unsigned char x[];  // [64][512]
+  extern __shared__ __align__(16) unsigned char x[];  // [kTileRows][kTileRowBytes]
   __shared__ __align__(16) uint8_t scales_r[W / 128][kTileRows][4];  // of the rows, 128 columns each
   __shared__ __align__(4) uint8_t scales_c[W][2];                     // of the columns, this CTA's two blocks
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -474,10 +478,13 @@ cudaError_t quantize_dt(const QuantParams &p, cudaStream_t s) {
   if constexpr (!kTiled) if (!cols && !tiled) {
     const long long grid = ceil_div(p.rows, (long long)kMx4TileRows) * p.by_rows.tiles_k;
     // More warps a tile where tiles are few.  To nearest: sixteen below two
-    // tiles an SM, else eight (8192 x 4096 bfloat16: 14.4 us, 16.4 with four);
-    // the kernels that call the generator hold 110 registers a thread and
-    // want about twelve warps an SM (stochastic 2048 x 4096: 9.7 us with eight warps a
-    // tile, 11.2 with sixteen, 12.0 with four).
+    // tiles an SM (binary32 1024 x 4096: 4.7 us, 5.9 with eight, 8.8 with four),
+    // else eight (8192 x 4096: bfloat16 14.3 us, 16.1 with sixteen, 16.6 with four;
+    // binary32 24.3, 24.7 and 25.8).  The kernels that call the generator hold 110
+    // registers a thread and want about twelve warps an SM (binary32 stochastic
+    // 8192 x 4096: 29.5 us with four warps a tile, 30.6 with eight, 38.5 with
+    // sixteen; bfloat16 1024 x 4096 stochastic with dropout: 7.4 us with sixteen, 8.4
+    // with eight, 13.8 with four).
     int threads = 128;
     if constexpr (SR || DROP) {
       while (threads < 512 && grid * threads < 12 * 32ll * p.sms) threads *= 2;

@@ -513,6 +513,48 @@ rr_status ring_mx4_matmul(const rr_mx4 *a, const rr_mx4 *b, void *out, size_t ld
  */
 rr_status ring_mx4_allreduce(const rr_mx4 *in, void *const *out_bufs, int R, rr_dtype dtype, cudaStream_t stream);
 
+/*
+ * The operators of a training step around the products: the norm before one
+ * (ring_layer_norm), the loss after the last one (ring_linear_cross_entropy)
+ * and the update made of the summed gradients (ring_orthogonalize).  They follow
+ * the common rules of the calls above: asynchronous on `stream`, arguments checked
+ * first, no allocation (a workspace is the caller's: device memory, 16-byte
+ * aligned, of the size that the function beside the call gives; its contents mean
+ * nothing before or after the call, and two calls that may run at once need one
+ * each), programmatic launch, any ld >= cols and any element-aligned address.
+ * rows and cols are below 2^31 - 256.  Results do not depend on timing.
+ */
+
+/*
+ * ring_layer_norm -- for each row of x (rows x cols):
+ *   out = (x - mean) * rstd * weight + bias,
+ *   mean = sum(x) / cols, rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps),
+ * in binary32, one rounding to storage.  weight and bias: cols elements of wtype
+ * (dtype or RR_FP32) each, or NULL (1 and 0).  mean and rstd: binary32, one a
+ * row, for the backward pass, or NULL.  eps >= 0.  out may be x (same address
+ * and ld) or lie beside it in the rows of one array (same ld); any other overlap
+ * is RR_ERR_ALIAS.
+ */
+rr_status ring_layer_norm(const void *x, size_t ld_x, const void *weight, const void *bias, rr_dtype wtype, double eps,
+                          void *out, size_t ld_out, float *mean, float *rstd, size_t rows, size_t cols, rr_dtype dtype,
+                          cudaStream_t stream);
+
+/*
+ * ring_layer_norm_backward -- with h = (x - mean) * rstd and g = dy * weight:
+ *   dx = (g - sum(g) / cols - h * sum(g h) / cols) * rstd for each row,
+ *   dweight = sum over rows of dy h, dbias = sum over rows of dy (of wtype).
+ * mean and rstd as ring_layer_norm gave them.  dx, dweight and dbias: NULL for
+ * what is not wanted; with no rows dweight and dbias are 0.  dx may be dy or x
+ * (same address and ld) or lie beside them in the rows of one array.  workspace:
+ * ring_layer_norm_workspace(rows, cols) bytes if dweight or dbias is wanted (0
+ * bytes with no rows).
+ */
+size_t ring_layer_norm_workspace(size_t rows, size_t cols);
+rr_status ring_layer_norm_backward(const void *dy, size_t ld_dy, const void *x, size_t ld_x, const void *weight,
+                                   rr_dtype wtype, const float *mean, const float *rstd, void *dx, size_t ld_dx,
+                                   void *dweight, void *dbias, size_t rows, size_t cols, rr_dtype dtype, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+
 /* RR_ABI_VERSION of the library. */
 int ring_abi_version(void);
 

@@ -17,6 +17,8 @@ import torch
 from . import mx4 as _mx4
 from .mx4 import (Dropout, Mx4, dropout, mx4_allreduce, mx4_dequantize, mx4_linear, mx4_matmul, mx4_quantize,
                   mx4_quantize_both)
+from . import training as _training
+from .training import layer_norm, layer_norm_backward, layer_norm_forward
 
 __all__ = [
     "RingError", "lib", "allreduce", "reduce_scatter", "allgather", "collective", "plan",
@@ -25,6 +27,7 @@ __all__ = [
     "debug_checks", "debug_set_margin", "HOST_COPIES_OVERLAP", "HOST_COPIES_ONE_WAY",
     "Mx4", "Dropout", "mx4_quantize", "mx4_quantize_both", "mx4_dequantize", "mx4_matmul", "mx4_allreduce",
     "mx4_linear", "dropout",
+    "layer_norm", "layer_norm_forward", "layer_norm_backward",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_ALIAS", "ERR_CUDA", "ERR_TIMEOUT",
     "OP_ALLREDUCE", "OP_REDUCE_SCATTER", "OP_ALLGATHER", "PATH_AUTO", "PATH_BULK", "PATH_SIMPLE", "PATH_DIRECT",
 ]
@@ -150,6 +153,7 @@ def lib() -> ctypes.CDLL:
         L.ring_debug_set_margin.argtypes = [sz]
         L.ring_debug_set_margin.restype = i
         _mx4.bind(L)
+        _training.bind(L)
         _lib = L
     return _lib
 

@@ -3,52 +3,22 @@
 // call, and the parameter blocks of the launches.
 #include <math.h>
 
+#include "rr_args.h"
 #include "rr_mx4.h"
 
 namespace {
 
+using rr::aligned16;
+using rr::aligned32;
 using rr::ceil_div;
+using rr::elem_bytes;
+using rr::matrix_span;
+using rr::share;
+using rr::Span;
+using rr::span_of;
+using rr::valid_type;
 
 constexpr size_t kMaxExtent = 0x7fffff00;  // rows or columns (tensor-copy coordinates are 32 bits)
-
-size_t elem_bytes(int t) { return t == RR_FP32 ? 4 : 2; }
-bool valid_type(int t) { return t == RR_FP32 || t == RR_FP16 || t == RR_BF16; }
-
-struct Span {
-  uintptr_t lo = 0, hi = 0;
-  bool overlaps(const Span &o) const { return lo < hi && o.lo < o.hi && lo < o.hi && o.lo < hi; }
-};
-
-bool span_of(const void *ptr, size_t bytes, size_t align, Span *s) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(ptr);
-  if (bytes == 0) return *s = Span{}, true;
-  if (a == 0 || a % align != 0 || a > UINTPTR_MAX - bytes) return false;
-  *s = Span{a, a + bytes};
-  return true;
-}
-
-// A strided matrix: its extent, and whether 16-byte groups of its rows are aligned.
-bool matrix_span(const void *ptr, size_t rows, size_t cols, size_t ld, size_t E, Span *s) {
-  if (rows == 0 || cols == 0) return *s = Span{}, true;
-  if (ld < cols || ld > (SIZE_MAX / 8) / E / rows) return false;
-  return span_of(ptr, ((rows - 1) * ld + cols) * E, E, s);
-}
-// Whether two strided matrices of rows x cols share an element.  Of one ld they
-// may lie beside one another in the rows of one array: the second begins `at`
-// bytes into a row of the first, past its last column, and ends in that row.
-bool share(const Span &a, size_t ld_a, const Span &b, size_t ld_b, size_t cols, size_t E) {
-  if (!a.overlaps(b)) return false;
-  if (ld_a != ld_b) return true;
-  const size_t row = ld_a * E, apart = a.lo < b.lo ? (b.lo - a.lo) % row : row - (a.lo - b.lo) % row, at = apart % row;
-  return at < cols * E || at + cols * E > row;
-}
-bool aligned16(const void *ptr, size_t rows, size_t ld, size_t E) {
-  return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && (rows <= 1 || ld * E % 16 == 0);
-}
-
-bool aligned32(const void *ptr, size_t rows, size_t ld, size_t E) {
-  return reinterpret_cast<uintptr_t>(ptr) % 32 == 0 && (rows <= 1 || ld * E % 32 == 0);
-}
 
 bool extents_ok(size_t rows, size_t cols) {
   return rows <= kMaxExtent && cols <= kMaxExtent && (cols == 0 || rows <= (SIZE_MAX / 64) / cols);

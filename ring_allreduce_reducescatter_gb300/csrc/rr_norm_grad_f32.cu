@@ -1,0 +1,8 @@
+// Layer norm backward of one storage format.
+#include "rr_norm.cuh"
+
+namespace rr {
+cudaError_t launch_norm_grad_f32(const NormGradParams &p, cudaStream_t s) {
+  return p.wtype == kF32 ? norm::backward<kF32, kF32>(p, s) : norm::backward<kF32, kF32>(p, s);
+}
+}  // namespace rr

@@ -555,6 +555,50 @@ rr_status ring_layer_norm_backward(const void *dy, size_t ld_dy, const void *x, 
                                    void *dweight, void *dbias, size_t rows, size_t cols, rr_dtype dtype, void *workspace,
                                    size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * ring_linear_cross_entropy -- the softmax cross entropy of logits l = x w^T (x:
+ * tokens x hidden, w: vocabulary x hidden, both dtype, RR_FP16 or RR_BF16;
+ * RR_FP32 is RR_ERR_UNSUPPORTED) against one target a token, without storing the
+ * logits:
+ *   lse[t] = log(sum over v of exp(l[t][v])), loss[t] = lse[t] - l[t][target[t]],
+ * sums and exponentials in binary32.  A token whose target is ignore_index has
+ * loss 0 and counts nothing; any other target outside 0 .. vocabulary - 1 makes
+ * its loss (and in the backward pass dw, and its row of dx) NaN.  Logits that are
+ * not finite give NaN.  lse (for the backward pass) and sums may be NULL; sums:
+ * three values, the total of the losses, how many tokens count, and their mean (0
+ * if none does).  hidden and vocabulary are 1 or more.  workspace:
+ * ring_linear_cross_entropy_workspace of the same x, w and sizes; it holds a copy
+ * of x or w if its rows are not 16-byte aligned, and of an x of few short rows.
+ */
+size_t ring_linear_cross_entropy_workspace(const void *x, size_t ld_x, const void *w, size_t ld_w, size_t tokens, size_t hidden,
+                                           size_t vocabulary);
+rr_status ring_linear_cross_entropy(const void *x, size_t ld_x, const void *w, size_t ld_w, const long long *target,
+                                    long long ignore_index, float *loss, float *lse, float *sums, size_t tokens, size_t hidden,
+                                    size_t vocabulary, rr_dtype dtype, void *workspace, size_t workspace_bytes,
+                                    cudaStream_t stream);
+
+/*
+ * ring_linear_cross_entropy_backward -- with grad[t * grad_step] the gradient
+ * that token t's loss has (grad_step 0: one for all, 1: one each) and p the
+ * softmax of its logits (made again from x and w, and lse as the forward pass
+ * gave it):
+ *   e[t][v] = grad (p[t][v] - (v == target[t])), 0 for a token that counts nothing,
+ *   dx = e w, dw = e^T x
+ * of dtype; NULL for what is not wanted.  e is rounded to dtype (times a power of
+ * two of the gradients' own, so that it neither overflows nor underflows) and held
+ * for a piece of the vocabulary at a time, 256 MiB at most (or 256 columns); sums
+ * in binary32, each output rounded once.  x must be finite also where a token
+ * counts nothing (0 times what is not finite is not 0 in dw).  workspace:
+ * ring_linear_cross_entropy_backward_workspace of the same x, w and sizes.
+ */
+size_t ring_linear_cross_entropy_backward_workspace(const void *x, size_t ld_x, const void *w, size_t ld_w, size_t tokens,
+                                                    size_t hidden, size_t vocabulary);
+rr_status ring_linear_cross_entropy_backward(const float *grad, size_t grad_step, const void *x, size_t ld_x, const void *w,
+                                             size_t ld_w, const long long *target, long long ignore_index, const float *lse,
+                                             void *dx, size_t ld_dx, void *dw, size_t ld_dw, size_t tokens, size_t hidden,
+                                             size_t vocabulary, rr_dtype dtype, void *workspace, size_t workspace_bytes,
+                                             cudaStream_t stream);
+
 /* RR_ABI_VERSION of the library. */
 int ring_abi_version(void);
 

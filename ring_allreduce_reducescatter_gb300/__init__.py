@@ -18,7 +18,8 @@ from . import mx4 as _mx4
 from .mx4 import (Dropout, Mx4, dropout, mx4_allreduce, mx4_dequantize, mx4_linear, mx4_matmul, mx4_quantize,
                   mx4_quantize_both)
 from . import training as _training
-from .training import layer_norm, layer_norm_backward, layer_norm_forward
+from .training import (layer_norm, layer_norm_backward, layer_norm_forward, linear_cross_entropy,
+                       linear_cross_entropy_backward, linear_cross_entropy_forward)
 
 __all__ = [
     "RingError", "lib", "allreduce", "reduce_scatter", "allgather", "collective", "plan",
@@ -28,6 +29,7 @@ __all__ = [
     "Mx4", "Dropout", "mx4_quantize", "mx4_quantize_both", "mx4_dequantize", "mx4_matmul", "mx4_allreduce",
     "mx4_linear", "dropout",
     "layer_norm", "layer_norm_forward", "layer_norm_backward",
+    "linear_cross_entropy", "linear_cross_entropy_forward", "linear_cross_entropy_backward",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_ALIAS", "ERR_CUDA", "ERR_TIMEOUT",
     "OP_ALLREDUCE", "OP_REDUCE_SCATTER", "OP_ALLGATHER", "PATH_AUTO", "PATH_BULK", "PATH_SIMPLE", "PATH_DIRECT",
 ]

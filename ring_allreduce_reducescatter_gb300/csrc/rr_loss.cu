@@ -1,0 +1,237 @@
+// rr_loss.cu -- the softmax cross entropy of logits l = x W^T that are never
+// stored:
+//   lse[t] = log(sum_v exp(l[t, v])), loss[t] = lse[t] - l[t, target[t]].
+// The product's epilogue keeps, of a row and 128 (64) columns, the maximum and
+// the sum of exponentials around it, 8 bytes for 256 of logits, and the target's
+// logit where it passes; loss_rows_kernel joins them.  The product bounds it: for
+// 8192 tokens by 32000 by 4096, 2.1 TFLOP of tensor work for 16 MB of sums.
+#include <math.h>
+
+#include "rr_gemm.cuh"
+#include "rr_loss.h"
+
+namespace rr {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// exp(a - b) for b >= a or b finite: 0 where a is minus infinity, whatever b.
+__device__ __forceinline__ float exp_above(float a, float b) {
+  return a == -INFINITY ? 0.f : ex2(__fmul_rn(__fsub_rn(a, b), kLog2e));
+}
+
+struct Statistics {
+  struct Params {
+    const long long *target;
+    float2 *parts;
+    float *chosen;
+    long long tokens, vocabulary, group;
+  };
+  const Params &p;
+  long long row, col, at;
+  float top, sum;
+  __device__ __forceinline__ Statistics(const Params &p, long long row, long long col, int, float *)
+      : p(p), row(row), col(col), at(row < p.tokens ? p.target[row] : -1), top(-INFINITY), sum(0.f) {}
+  // One pass with a running maximum: the sum so far is scaled down where it rises.
+  __device__ __forceinline__ void chunk(int c, float v[gemm::kChunk]) {
+    const long long first = col + c * gemm::kChunk;
+    if (first >= p.vocabulary) return;
+    if (at >= first && at < first + gemm::kChunk && at < p.vocabulary) {
+      const int j0 = (int)(at - first);
+#pragma unroll
+      for (int j = 0; j < gemm::kChunk; ++j)
+        if (j == j0) p.chosen[row] = v[j];
+    }
+    if (first + gemm::kChunk > p.vocabulary) {
+#pragma unroll
+      for (int j = 0; j < gemm::kChunk; ++j) v[j] = first + j < p.vocabulary ? v[j] : -INFINITY;
+    }
+    float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int j = 4; j < gemm::kChunk; ++j) m[j % 4] = fmaxf(m[j % 4], v[j]);
+    const float high = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    if (high > top) sum = __fmul_rn(sum, exp_above(top, high)), top = high;
+    // (with nothing above minus infinity yet, every term is 0: around 0, not around top)
+    const float around = top == -INFINITY ? 0.f : top;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < gemm::kChunk; ++j) s[j % 4] = __fadd_rn(s[j % 4], ex2(__fmul_rn(__fsub_rn(v[j], around), kLog2e)));
+    sum = __fadd_rn(sum, __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])));
+  }
+  __device__ __forceinline__ void end() {
+    if (row < p.tokens && col < p.vocabulary) p.parts[col / p.group * p.tokens + row] = make_float2(top, sum);
+  }
+};
+
+// The groups of a row joined: kRows rows a CTA of 256 threads, 256 / kRows
+// threads each a part of a row's groups, joined in a fixed tree (one thread that
+// joined 256 parts in turn took 12 us).
+struct Part {
+  float top, sum;
+  __device__ __forceinline__ void join(float top2, float sum2) {
+    if (top2 > top) sum = __fmul_rn(sum, exp_above(top, top2)), top = top2;
+    // (a sum that is no number stays one, whatever its maximum)
+    sum = sum2 == sum2 ? __fadd_rn(sum, __fmul_rn(sum2, exp_above(top2, top))) : sum2;
+  }
+};
+template <int kRows>
+__global__ void __launch_bounds__(256) loss_rows_kernel(const __grid_constant__ LossParams p, long long groups) {
+  constexpr int kEach = 256 / kRows;
+  __shared__ Part got[8][kRows];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int r = threadIdx.x % kRows, g0 = threadIdx.x / kRows;
+  const long long row = (long long)blockIdx.x * kRows + r, tokens = p.x.rows;
+  Part v{-INFINITY, 0.f};
+  if (row < tokens) {
+#pragma unroll 4
+    for (long long g = g0; g < groups; g += kEach) {
+      const float2 w = p.parts[g * tokens + row];
+      v.join(w.x, w.y);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d >= kRows; d /= 2) {
+    const float top = __shfl_xor_sync(0xffffffffu, v.top, d), sum = __shfl_xor_sync(0xffffffffu, v.sum, d);
+    v.join(top, sum);
+  }
+  if (threadIdx.x % 32 < kRows) got[threadIdx.x / 32][r] = v;
+  __syncthreads();
+  if (g0 != 0 || row >= tokens) return;
+#pragma unroll
+  for (int q = 1; q < 8; ++q) v.join(got[q][r].top, got[q][r].sum);
+  const float lse = v.top == -INFINITY ? (v.sum == v.sum ? -INFINITY : v.sum) : __fadd_rn(v.top, logf(v.sum));
+  const long long t = p.target[row];
+  const bool valid = t >= 0 && t < p.w.rows;
+  if (p.lse) p.lse[row] = lse;
+  p.loss[row] = t == p.ignore ? 0.f : valid ? __fsub_rn(lse, p.chosen[row]) : NAN;
+}
+
+// sums: the losses' total, how many tokens count, and the mean over those (0
+// with none), by one CTA in a fixed order.
+__global__ void __launch_bounds__(1024) loss_sums_kernel(const __grid_constant__ LossParams p) {
+  __shared__ float totals[32];
+  __shared__ int counts[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  float total = 0.f;
+  int count = 0;
+#pragma unroll 4
+  for (long long t = threadIdx.x; t < p.x.rows; t += 1024) {
+    total = __fadd_rn(total, p.loss[t]);
+    count += p.target[t] != p.ignore;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) {
+    total = __fadd_rn(total, __shfl_xor_sync(0xffffffffu, total, d));
+    count += __shfl_xor_sync(0xffffffffu, count, d);
+  }
+  if (threadIdx.x % 32 == 0) totals[threadIdx.x / 32] = total, counts[threadIdx.x / 32] = count;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 32; ++w) total = __fadd_rn(total, totals[w]), count += counts[w];
+  p.sums[0] = total, p.sums[1] = (float)count;
+  p.sums[2] = count ? __fdiv_rn(total, (float)count) : 0.f;
+}
+
+// What each token's loss passes on, as the factor of its row of the logits'
+// gradient, 0 for a token that does not count and NaN for a target outside the
+// vocabulary; and the factor of the outputs.  One gradient for all tokens goes to
+// the outputs whole, so that e is p - 1 and p themselves (their common factor
+// rounded into every e put the same error, up to half a step, on all of them: twice
+// the error of dx).  Gradients of their own go over a common power of two, that of
+// the largest.  In binary16 e is 2^14 times as large: it neither overflows nor
+// falls among the subnormals, down to probabilities of 2^-28.
+__global__ void __launch_bounds__(1024) loss_factors_kernel(const __grid_constant__ LossGradParams p) {
+  __shared__ float tops[32];
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const long long tokens = p.x.rows;
+  const float widen = p.dtype == kF16 ? 16384.f : 1.f;
+  float down = widen, up = 1.f;
+  if (p.grad_step == 0) {
+    up = __fdiv_rn(p.grad[0], widen);
+  } else {
+    float top = 0.f;
+#pragma unroll 4
+    for (long long t = threadIdx.x; t < tokens; t += 1024)
+      if (p.target[t] != p.ignore) top = fmaxf(top, fabsf(p.grad[t]));
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
+    __syncthreads();
+    for (int w = 0; w < 32; ++w) top = fmaxf(top, tops[w]);
+    // 2^k with top <= 2^k, k in -100 .. 100; 1 where there is nothing to scale
+    int k = 0;
+    if (top > 0.f && top < INFINITY) frexpf(top, &k);
+    k = k < -100 ? -100 : k > 100 ? 100 : k;
+    down = __fmul_rn(__int_as_float((127 - k) << 23), widen), up = __fdiv_rn(__int_as_float((127 + k) << 23), widen);
+  }
+#pragma unroll 4
+  for (long long t = threadIdx.x; t < tokens; t += 1024) {
+    const long long at = p.target[t];
+    const float g = p.grad_step == 0 ? widen : __fmul_rn(p.grad[t], down);
+    p.factors[t] = at == p.ignore ? 0.f : at >= 0 && at < p.w.rows ? g : NAN;
+  }
+  if (threadIdx.x == 0) p.factors[tokens] = up;
+}
+
+// A copy in rows of ld_to, for operands that tensor copies do not read as they lie.
+__global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ PadParams p) {
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const uint16_t *from = static_cast<const uint16_t *>(p.from);
+  uint16_t *to = static_cast<uint16_t *>(p.to);
+  for (long long row = blockIdx.x; row < p.rows_to; row += gridDim.x) {
+    const long long cols = row < p.rows ? p.cols : 0;
+#pragma unroll 4
+    for (long long c = threadIdx.x; c < p.ld_to; c += 256) to[row * p.ld_to + c] = c < cols ? from[row * p.ld_from + c] : (uint16_t)0;
+  }
+}
+
+template <class... P, class... Args>
+cudaError_t launch(void (*k)(P...), long long grid, int block, cudaStream_t s, const Args &...args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3((unsigned)block);
+  c.stream = s;
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, k, args...);
+}
+
+}  // namespace
+
+cudaError_t launch_pad(const PadParams &p, cudaStream_t s) {
+  return launch(pad_kernel, p.rows_to < 8192 ? p.rows_to : 8192, 256, s, p);
+}
+
+cudaError_t launch_loss(const LossParams &p, cudaStream_t s) {
+  const long long tokens = p.x.rows, vocabulary = p.w.rows, group = loss_group(tokens), groups = ceil_div(vocabulary, group);
+  if (tokens == 0) return launch(loss_sums_kernel, 1, 1024, s, p);
+  const gemm::Operand a{p.x.at, p.x.padded, p.hidden, p.x.ld, 0, 1, false}, b{p.w.at, vocabulary, p.hidden, p.w.ld, 0, 1, false};
+  const Statistics::Params e{p.target, p.parts, p.chosen, tokens, vocabulary, group};
+  cudaError_t err = gemm::launch_product<false, false, Statistics>(a, b, false, loss_pairs(tokens), p.dtype == kBF16, p.status,
+                                                                   p.sms, e, s);
+  if (err != cudaSuccess) return err;
+  // few rows: a CTA on each (one token of 131072 has 2048 groups)
+  err = tokens <= 4 * p.sms ? launch(loss_rows_kernel<1>, tokens, 256, s, p, groups)
+                            : launch(loss_rows_kernel<8>, ceil_div(tokens, 8ll), 256, s, p, groups);
+  if (err != cudaSuccess || !p.sums) return err;
+  return launch(loss_sums_kernel, 1, 1024, s, p);
+}
+
+cudaError_t launch_loss_factors(const LossGradParams &p, cudaStream_t s) {
+  return launch(loss_factors_kernel, 1, 1024, s, p);
+}
+
+}  // namespace rr

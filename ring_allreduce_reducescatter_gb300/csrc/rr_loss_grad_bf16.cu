@@ -1,0 +1,6 @@
+// The linear cross entropy's gradient of one storage format.
+#include "rr_loss_grad.cuh"
+
+namespace rr {
+cudaError_t launch_loss_grad_bf16(const LossGradParams &p, cudaStream_t s) { return loss::backward<kBF16>(p, s); }
+}  // namespace rr

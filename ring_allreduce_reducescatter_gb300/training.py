@@ -25,7 +25,13 @@ def bind(L) -> None:
     L.ring_layer_norm_workspace.argtypes, L.ring_layer_norm_workspace.restype = [sz, sz], sz
     L.ring_layer_norm.argtypes = [vp, sz, vp, vp, i, f64, vp, sz, vp, vp, sz, sz, i, vp]
     L.ring_layer_norm_backward.argtypes = [vp, sz, vp, sz, vp, i, vp, vp, vp, sz, vp, vp, sz, sz, i, vp, sz, vp]
-    for f in ("ring_layer_norm", "ring_layer_norm_backward"):
+    i64 = ctypes.c_longlong
+    for f in ("ring_linear_cross_entropy_workspace", "ring_linear_cross_entropy_backward_workspace"):
+        getattr(L, f).argtypes, getattr(L, f).restype = [vp, sz, vp, sz, sz, sz, sz], sz
+    L.ring_linear_cross_entropy.argtypes = [vp, sz, vp, sz, vp, i64, vp, vp, vp, sz, sz, sz, i, vp, sz, vp]
+    L.ring_linear_cross_entropy_backward.argtypes = [vp, sz, vp, sz, vp, sz, vp, i64, vp, vp, sz, vp, sz, sz, sz, sz, i, vp,
+                                                     sz, vp]
+    for f in ("ring_layer_norm", "ring_layer_norm_backward", "ring_linear_cross_entropy", "ring_linear_cross_entropy_backward"):
         getattr(L, f).restype = i
 
 
@@ -184,3 +190,122 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
             raise ValueError("out: a gradient is being recorded, and would be lost")
         return _Norm.apply(x, weight, bias, eps)
     return _norm(x, weight, bias, eps, out, False)[0]
+
+
+# ------------------------------------------------------- linear cross entropy
+
+
+def _loss_operands(x, w, target):
+    tokens, hidden, ld_x = _matrix(x, "x")
+    vocabulary, h, ld_w = _matrix(w, "w")
+    if h != hidden:
+        raise ValueError(f"x has {hidden} columns, w {h}")
+    if x.dtype != w.dtype or x.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"x is {x.dtype}, w {w.dtype}: both float16 or both bfloat16 are wanted")
+    if (not isinstance(target, torch.Tensor) or target.dtype != torch.int64 or tuple(target.shape) != (tokens,)
+            or not target.is_contiguous()):
+        raise ValueError(f"target: needs a contiguous int64 tensor of {tokens} elements")
+    if w.device != x.device or target.device != x.device:
+        raise ValueError("x, w and target must be on one device")
+    if hidden < 1 or vocabulary < 1:
+        raise ValueError("hidden size and vocabulary must not be empty")
+    return tokens, hidden, vocabulary, max(ld_x, hidden), max(ld_w, hidden), _dtype(x.dtype)
+
+
+def _losses(x, w, target, ignore_index, want_lse, want_sums):
+    """(loss, lse, sums), None for what is not wanted."""
+    tokens, hidden, vocabulary, ld_x, ld_w, code = _loss_operands(x, w, target)
+    device, handle, L = x.device, _current(x.device), _L or _lib()
+    loss = torch.empty(tokens, dtype=_F32, device=device)
+    lse = torch.empty(tokens, dtype=_F32, device=device) if want_lse else None
+    sums = torch.empty(3, dtype=_F32, device=device) if want_sums else None
+    at = (x.data_ptr(), ld_x, w.data_ptr(), ld_w)
+    need = L.ring_linear_cross_entropy_workspace(*at, tokens, hidden, vocabulary)
+    space = torch.empty(need, dtype=torch.uint8, device=device)
+    status = L.ring_linear_cross_entropy(*at, target.data_ptr(), ignore_index, loss.data_ptr(), _at(lse), _at(sums), tokens,
+                                         hidden, vocabulary, code, space.data_ptr(), need, handle)
+    if status:
+        _failed(status, "ring_linear_cross_entropy")
+    return loss, lse, sums
+
+
+def linear_cross_entropy_forward(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, ignore_index: int = -100,
+                                 stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(loss, lse) of every token, float32: the softmax cross entropy of the
+    logits x @ w.T, which are never stored, against target, and the logarithm of
+    the sum of their exponentials, as linear_cross_entropy_backward takes it.
+    Records no gradient (linear_cross_entropy does)."""
+    if stream is not None:
+        return _on(stream, linear_cross_entropy_forward, x, w, target, ignore_index)
+    if _recorded(x, w):
+        raise ValueError("a gradient is being recorded, and would be lost: linear_cross_entropy records it")
+    return _losses(x, w, target, ignore_index, True, False)[:2]
+
+
+def linear_cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
+                                  lse: torch.Tensor, ignore_index: int = -100, want_dx: bool = True, want_dw: bool = True,
+                                  stream=None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(dx, dw) for the gradient of the tokens' losses: grad, float32, one element
+    for all tokens or one each.  None for what is not wanted."""
+    if stream is not None:
+        return _on(stream, linear_cross_entropy_backward, grad, x, w, target, lse, ignore_index, want_dx, want_dw)
+    tokens, hidden, vocabulary, ld_x, ld_w, code = _loss_operands(x, w, target)
+    device = x.device
+    if (not isinstance(grad, torch.Tensor) or grad.dtype != _F32 or grad.device != device or not grad.is_contiguous()
+            or not (grad.numel() == 1 or tuple(grad.shape) == (tokens,))):
+        raise ValueError(f"grad: needs a contiguous float32 tensor of one element or of {tokens} on {device}")
+    if (not isinstance(lse, torch.Tensor) or lse.dtype != _F32 or lse.device != device or tuple(lse.shape) != (tokens,)
+            or not lse.is_contiguous()):
+        raise ValueError(f"lse: needs a contiguous float32 tensor of {tokens} elements on {device}")
+    handle, L = _current(device), _L or _lib()
+    dx = torch.empty((tokens, hidden), dtype=x.dtype, device=device) if want_dx else None
+    dw = torch.empty((vocabulary, hidden), dtype=x.dtype, device=device) if want_dw else None
+    at = (x.data_ptr(), ld_x, w.data_ptr(), ld_w)
+    need = L.ring_linear_cross_entropy_backward_workspace(*at, tokens, hidden, vocabulary)
+    space = torch.empty(need, dtype=torch.uint8, device=device)
+    status = L.ring_linear_cross_entropy_backward(grad.data_ptr(), 0 if grad.numel() == 1 else 1, *at, target.data_ptr(),
+                                                  ignore_index, lse.data_ptr(), _at(dx), hidden, _at(dw), hidden, tokens, hidden,
+                                                  vocabulary, code, space.data_ptr(), need, handle)
+    if status:
+        _failed(status, "ring_linear_cross_entropy_backward")
+    return dx, dw
+
+
+_REDUCTIONS = {"none": None, "sum": 0, "mean": 2}
+
+
+class _CrossEntropy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, target, ignore_index, reduction):
+        loss, lse, sums = _losses(x, w, target, ignore_index, True, reduction != "none")
+        ctx.save_for_backward(x, w, target, lse, sums)
+        ctx.ignore_index, ctx.reduction = ignore_index, reduction
+        return loss if sums is None else sums[_REDUCTIONS[reduction]].clone()
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, w, target, lse, sums = ctx.saved_tensors
+        grad = dy.contiguous()
+        if ctx.reduction == "mean":
+            grad = grad / sums[1].clamp(min=1)
+        need = ctx.needs_input_grad
+        return linear_cross_entropy_backward(grad, x, w, target, lse, ctx.ignore_index, need[0], need[1]) + (None, None, None)
+
+
+def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor, ignore_index: int = -100,
+                         reduction: str = "mean", stream=None) -> torch.Tensor:
+    """The softmax cross entropy of the logits x @ w.T (x: [tokens, hidden], w:
+    [vocabulary, hidden], float16 or bfloat16) against target (int64, one a
+    token), differentiable in x and w; neither the logits nor their gradient is
+    ever stored whole.  A token whose target is ignore_index counts nothing.
+    reduction: "mean" over the tokens that count (0 if none does), "sum", or
+    "none" (each token's, 0 for one that does not count); float32."""
+    if reduction not in _REDUCTIONS:
+        raise ValueError(f"reduction {reduction!r}: 'mean', 'sum' or 'none' is wanted")
+    if stream is not None:
+        return _on(stream, linear_cross_entropy, x, w, target, ignore_index, reduction)
+    if isinstance(x, torch.Tensor) and isinstance(w, torch.Tensor) and _recorded(x, w):
+        return _CrossEntropy.apply(x, w, target, ignore_index, reduction)
+    loss, _, sums = _losses(x, w, target, ignore_index, False, reduction != "none")
+    return loss if sums is None else sums[_REDUCTIONS[reduction]]

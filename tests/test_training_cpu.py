@@ -86,3 +86,74 @@ def test_layer_norm_backward_refusals(L):
     assert call(rows=1 << 31) == EINVAL
     assert call(dx=dy + 2) == EALIAS and call(dx=x, ldd=97) == EALIAS and call(dw=db) == EALIAS and call(ws=x) == EALIAS
     assert call(dw=dy) == EALIAS and call(dx=w) == EALIAS and call(db=ws) == EALIAS and call(dw=m) == EALIAS
+
+
+# ------------------------------------------------------- linear cross entropy
+
+
+def test_cross_entropy_by_hand():
+    x, w = torch.eye(2), torch.tensor([[0.0, 1.0], [0.0, 0.0], [0.0, 0.0]])
+    loss, lse, _ = ref.cross_entropy(x, w, torch.tensor([2, -100]), -100)
+    assert abs(loss[0].item() - torch.log(torch.tensor(3.0, dtype=torch.float64)).item()) < 1e-12 and loss[1] == 0
+
+
+def test_cross_entropy_gradient_against_differences():
+    g = torch.Generator().manual_seed(1)
+    x, w = (torch.randn(s, generator=g).double() for s in ((6, 5), (9, 5)))
+    target, grad = torch.tensor([3, -100, 0, 8, 8, 2]), torch.rand(6, generator=g).double()
+    e = ref.cross_entropy_grad(grad, x @ w.t(), target, -100)
+    for d, at in ((e @ w, 0), (e.t() @ x, 1)):
+        v = torch.randn(d.shape, generator=g).double()
+
+        def loss(step):
+            args = [x, w]
+            args[at] = args[at] + step
+            return (ref.cross_entropy(*args, target, -100)[0] * grad).sum().item()
+
+        assert abs(slope(loss, v) - (d * v).sum().item()) < 1e-6
+
+
+def test_linear_cross_entropy_refusals(L):
+    x, w, t, loss, lse, sums, ws = (BASE + k * 16 * MB for k in range(7))
+    need = L.ring_linear_cross_entropy_workspace(x, 96, w, 96, 200, 96, 1000)
+    assert L.ring_linear_cross_entropy_workspace(x + 2, 96, w, 96, 200, 96, 1000) == need  # (few rows: x is copied in any case)
+    assert L.ring_linear_cross_entropy_workspace(x, 96, w, 99, 200, 96, 1000) == need + 1000 * 96 * 2
+    assert L.ring_linear_cross_entropy_workspace(x, 96, w, 96, 200, 0, 1000) == 0
+
+    def call(x=x, ldx=96, w=w, ldw=96, t=t, loss=loss, lse=lse, sums=sums, n=200, h=96, v=1000, dtype=BF16, ws=ws, wb=need):
+        return L.ring_linear_cross_entropy(x, ldx, w, ldw, t, -100, loss, lse, sums, n, h, v, dtype, ws, wb, None)
+
+    assert call() == ECUDA and call(lse=None, sums=None) == ECUDA and call(dtype=F16) == ECUDA
+    assert call(n=0, sums=None) == OK and call(n=0, ws=None, wb=0) == ECUDA
+    assert call(dtype=F32) == EUNSUP and call(dtype=5) == EINVAL and call(h=0) == EINVAL and call(v=0) == EINVAL
+    assert call(x=None) == EINVAL and call(w=w + 1) == EINVAL and call(t=t + 4) == EINVAL and call(loss=None) == EINVAL
+    assert call(ldx=95) == EINVAL and call(ldw=95) == EINVAL and call(wb=need - 1) == EINVAL and call(ws=None) == EINVAL
+    assert call(n=1 << 31) == EINVAL and call(v=1 << 31) == EINVAL and call(ws=ws + 8) == EINVAL
+    assert call(loss=x) == EALIAS and call(lse=loss) == EALIAS and call(ws=w) == EALIAS and call(sums=t) == EALIAS
+    assert call(ws=loss) == EALIAS and call(sums=lse) == EALIAS
+
+
+def test_linear_cross_entropy_backward_refusals(L):
+    g, x, w, t, lse, dx, dw, ws = (BASE + k * 16 * MB for k in range(8))
+    need = L.ring_linear_cross_entropy_backward_workspace(x, 96, w, 96, 200, 96, 1000)
+
+    def call(g=g, step=0, x=x, ldx=96, w=w, ldw=96, t=t, lse=lse, dx=dx, lddx=96, dw=dw, lddw=96, n=200, h=96, v=1000,
+             dtype=BF16, ws=ws, wb=need):
+        return L.ring_linear_cross_entropy_backward(g, step, x, ldx, w, ldw, t, -100, lse, dx, lddx, dw, lddw, n, h, v, dtype, ws,
+                                                    wb, None)
+
+    assert call() == ECUDA and call(step=1) == ECUDA and call(dx=None) == ECUDA and call(dw=None) == ECUDA
+    assert call(dx=None, dw=None) == OK and call(n=0, dw=None) == OK and call(n=0, ws=None, wb=0) == ECUDA
+    assert call(dtype=F32) == EUNSUP and call(dtype=-1) == EINVAL and call(step=2) == EINVAL and call(h=0) == EINVAL
+    assert call(g=None) == EINVAL and call(lse=lse + 2) == EINVAL and call(t=None) == EINVAL and call(lddx=90) == EINVAL
+    assert call(dw=dw + 1) == EINVAL and call(wb=need - 1) == EINVAL and call(ws=ws + 4) == EINVAL
+    assert call(dx=x) == EALIAS and call(dw=w) == EALIAS and call(dx=dw) == EALIAS and call(ws=dx) == EALIAS
+    assert call(dw=lse) == EALIAS and call(ws=t) == EALIAS and call(dx=g) == EALIAS
+
+
+def test_pieces_stay_within_their_memory(L):
+    for tokens in (1, 200, 8192, 100_000, 1 << 20):
+        for vocabulary in (1, 500, 32000, 131072):
+            need = L.ring_linear_cross_entropy_backward_workspace(BASE, 4096, BASE, 4096, tokens, 4096, vocabulary)
+            rows = -(-tokens // 128) * 128
+            assert need <= max((1 << 28) + 512 * rows, 512 * rows) + tokens * 4096 * 4 + rows * 4096 * 2 * (tokens < 128) + 8 * rows + 4096

@@ -28,3 +28,20 @@ def norm_grad(dy, x, mean, rstd, weight):
     dx = (g - g.mean(-1, keepdim=True) - h * (g * h).mean(-1, keepdim=True)) * rstd.double().unsqueeze(-1)
     axes = tuple(range(dy.dim() - 1))
     return dx, (dy * h).sum(axes), dy.sum(axes)
+
+
+def cross_entropy(x, w, target, ignore_index):
+    """(loss, lse, logits)."""
+    l = x.double() @ w.double().t()
+    lse = torch.logsumexp(l, 1)
+    counts = target != ignore_index
+    at = torch.where(counts, target, 0)
+    return torch.where(counts, lse - l.gather(1, at[:, None]).squeeze(1), 0.0), lse, l
+
+
+def cross_entropy_grad(grad, l, target, ignore_index):
+    """e: the gradient of the logits; grad: one element, or one a token."""
+    counts = target != ignore_index
+    e = torch.softmax(l, 1)
+    e[torch.arange(l.shape[0], device=l.device), torch.where(counts, target, 0)] -= 1
+    return e * (torch.where(counts, 1.0, 0.0) * grad.double())[:, None]

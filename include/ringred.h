@@ -599,6 +599,28 @@ rr_status ring_linear_cross_entropy_backward(const float *grad, size_t grad_step
                                              size_t vocabulary, rr_dtype dtype, void *workspace, size_t workspace_bytes,
                                              cudaStream_t stream);
 
+/*
+ * ring_orthogonalize -- a matrix (an update made of summed gradients) brought near
+ * the orthogonal matrix that has its singular vectors, by Newton-Schulz steps:
+ *   X = G / (|G| + eps) in the Frobenius norm, then `steps` times
+ *   X <- a X + (b S + c S^2) X, S = X X^T (on the shorter side: with rows > cols
+ *   X <- a X + X (b S + c S^2), S = X^T X), (a, b, c) = (3.4445, -4.7750, 2.0315),
+ * of `batch` equal matrices at once (stride_g and stride_out elements from one to
+ * the next, of no meaning for one).  out may have another dtype than g.  X, S and
+ * the polynomial are held in binary16 (times powers of two that keep them inside
+ * its range), sums in binary32; out is rounded once.  Each step multiplies what
+ * the roundings before it left by up to 4.3, so that a matrix whose norm lies in a
+ * few directions a thousand times stronger than the rest keeps few digits of the
+ * rest.  A matrix of zeros gives zeros (with eps > 0); one that holds an infinity
+ * or a NaN gives NaN and leaves the others of the batch alone.  1 <= steps <= 1000,
+ * eps >= 0.  out may be g (same address, ld, stride and dtype).  batch up to 65535.
+ * workspace: ring_orthogonalize_workspace bytes, 32-byte aligned.
+ */
+size_t ring_orthogonalize_workspace(size_t batch, size_t rows, size_t cols);
+rr_status ring_orthogonalize(const void *g, size_t ld_g, size_t stride_g, rr_dtype dtype, void *out, size_t ld_out,
+                             size_t stride_out, rr_dtype out_dtype, size_t batch, size_t rows, size_t cols, int steps, double eps,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* RR_ABI_VERSION of the library. */
 int ring_abi_version(void);
 

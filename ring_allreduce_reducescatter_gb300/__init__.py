@@ -19,7 +19,7 @@ from .mx4 import (Dropout, Mx4, dropout, mx4_allreduce, mx4_dequantize, mx4_line
                   mx4_quantize_both)
 from . import training as _training
 from .training import (layer_norm, layer_norm_backward, layer_norm_forward, linear_cross_entropy,
-                       linear_cross_entropy_backward, linear_cross_entropy_forward)
+                       linear_cross_entropy_backward, linear_cross_entropy_forward, orthogonalize)
 
 __all__ = [
     "RingError", "lib", "allreduce", "reduce_scatter", "allgather", "collective", "plan",
@@ -29,7 +29,7 @@ __all__ = [
     "Mx4", "Dropout", "mx4_quantize", "mx4_quantize_both", "mx4_dequantize", "mx4_matmul", "mx4_allreduce",
     "mx4_linear", "dropout",
     "layer_norm", "layer_norm_forward", "layer_norm_backward",
-    "linear_cross_entropy", "linear_cross_entropy_forward", "linear_cross_entropy_backward",
+    "linear_cross_entropy", "linear_cross_entropy_forward", "linear_cross_entropy_backward", "orthogonalize",
     "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_ALIAS", "ERR_CUDA", "ERR_TIMEOUT",
     "OP_ALLREDUCE", "OP_REDUCE_SCATTER", "OP_ALLGATHER", "PATH_AUTO", "PATH_BULK", "PATH_SIMPLE", "PATH_DIRECT",
 ]

@@ -1,0 +1,35 @@
+// rr_orth.h -- parameter block and launcher of the orthogonalised update,
+// between the C ABI (rr_orth_api.cu) and the kernels (rr_orth.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "rr_mx4.h"
+
+namespace rr {
+
+struct OrthParams {
+  const void *g;
+  void *out;
+  long long rows, cols, ld_g, ld_out, stride_g, stride_out;  // strides: from matrix to matrix
+  int batch, steps, dtype, out_dtype;
+  float eps;
+  float *norms;       // [batch][kOrthParts][3]
+  void *x[2], *s, *b; // binary16: two iterates, the Gram matrix and its polynomial
+  long long held_rows, held_cols, ld_x, ld_s, stride_x, stride_s;
+  unsigned int *status;
+  int sms;
+};
+
+constexpr int kOrthParts = 256;  // partial sums of a matrix's squares
+
+// The sizes that the iterates are held in: small ones in whole boxes of zeros and
+// elements (rr_gemm.cuh says why).
+inline long long orth_held(long long n, long long rows, long long cols) {
+  return rows * cols * 2 < (1 << 20) ? ceil_div(n, 128ll) * 128 : n;
+}
+
+cudaError_t launch_orth(const OrthParams &p, cudaStream_t s);
+
+}  // namespace rr

@@ -31,7 +31,10 @@ def bind(L) -> None:
     L.ring_linear_cross_entropy.argtypes = [vp, sz, vp, sz, vp, i64, vp, vp, vp, sz, sz, sz, i, vp, sz, vp]
     L.ring_linear_cross_entropy_backward.argtypes = [vp, sz, vp, sz, vp, sz, vp, i64, vp, vp, sz, vp, sz, sz, sz, sz, i, vp,
                                                      sz, vp]
-    for f in ("ring_layer_norm", "ring_layer_norm_backward", "ring_linear_cross_entropy", "ring_linear_cross_entropy_backward"):
+    L.ring_orthogonalize_workspace.argtypes, L.ring_orthogonalize_workspace.restype = [sz, sz, sz], sz
+    L.ring_orthogonalize.argtypes = [vp, sz, sz, i, vp, sz, sz, i, sz, sz, sz, i, f64, vp, sz, vp]
+    for f in ("ring_layer_norm", "ring_layer_norm_backward", "ring_linear_cross_entropy", "ring_linear_cross_entropy_backward",
+              "ring_orthogonalize"):
         getattr(L, f).restype = i
 
 
@@ -309,3 +312,55 @@ def linear_cross_entropy(x: torch.Tensor, w: torch.Tensor, target: torch.Tensor,
         return _CrossEntropy.apply(x, w, target, ignore_index, reduction)
     loss, _, sums = _losses(x, w, target, ignore_index, False, reduction != "none")
     return loss if sums is None else sums[_REDUCTIONS[reduction]]
+
+
+# -------------------------------------------------------- orthogonalised update
+
+
+def _batch(t, name):
+    """(batch, rows, cols, row stride, matrix stride) of one matrix or a batch of
+    them, with neighbouring columns."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 3:
+        b, m, n = t.shape
+        if t.numel() == 0:
+            return b, m, n, n, m * n
+        _, _, ld = _matrix(t[0], name)
+        if b > 1 and t.stride(0) < (m - 1) * ld + n:
+            raise ValueError(f"{name}: the matrices of a batch must not overlap")
+        return b, m, n, ld, t.stride(0)
+    m, n, ld = _matrix(t, name)
+    return 1, m, n, ld, 0
+
+
+def orthogonalize(g: torch.Tensor, steps: int = 5, eps: float = 1e-7, dtype: Optional[torch.dtype] = None,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The matrix g, or each of a batch [batch, rows, cols], brought near the
+    orthogonal matrix that has its singular vectors by Newton-Schulz steps with
+    the coefficients (3.4445, -4.7750, 2.0315), which take every singular value
+    to about one; the step of the Muon optimiser, for the sum of the ranks'
+    gradients.  dtype: of the result (g's if None, or that of ``out``, which may
+    be g).  Records no gradient, so none may be wanted of g."""
+    if stream is not None:
+        return _on(stream, orthogonalize, g, steps, eps, dtype, out)
+    b, m, n, ld, stride = _batch(g, "g")
+    if _recorded(g):
+        raise ValueError("g: a gradient is being recorded, and would be lost")
+    code, device, handle = _dtype(g.dtype), g.device, _current(g.device)
+    if out is None:
+        out = torch.empty(g.shape, dtype=g.dtype if dtype is None else dtype, device=device)
+        ld_out, stride_out = n, m * n
+    else:
+        if not isinstance(out, torch.Tensor) or out.shape != g.shape or out.device != device:
+            raise ValueError("out must have g's shape and device")
+        if dtype not in (None, out.dtype):
+            raise ValueError(f"out: {out.dtype}, expected {dtype}")
+        _, _, _, ld_out, stride_out = _batch(out, "out")
+    out_code = _dtype(out.dtype)
+    L = _L or _lib()
+    need = L.ring_orthogonalize_workspace(b, m, n)
+    space = torch.empty(need, dtype=torch.uint8, device=device)
+    status = L.ring_orthogonalize(g.data_ptr(), ld, stride, code, out.data_ptr(), ld_out, stride_out, out_code, b, m, n, steps,
+                                  eps, space.data_ptr(), need, handle)
+    if status:
+        _failed(status, "ring_orthogonalize")
+    return out

@@ -157,3 +157,48 @@ def test_pieces_stay_within_their_memory(L):
             need = L.ring_linear_cross_entropy_backward_workspace(BASE, 4096, BASE, 4096, tokens, 4096, vocabulary)
             rows = -(-tokens // 128) * 128
             assert need <= max((1 << 28) + 512 * rows, 512 * rows) + tokens * 4096 * 4 + rows * 4096 * 2 * (tokens < 128) + 8 * rows + 4096
+
+
+# -------------------------------------------------------- orthogonalised update
+
+
+def test_orthogonal_by_singular_values():
+    g = torch.Generator().manual_seed(1)
+    for shape in ((7, 12), (12, 7), (9, 9)):
+        x = torch.randn(shape, generator=g).double()
+        u, s, v = torch.linalg.svd(x, full_matrices=False)
+        a, b, c = ref.QUINTIC
+        t = s / s.norm()
+        for _ in range(5):
+            t = a * t + b * t ** 3 + c * t ** 5
+        assert (ref.orthogonal(x, 5, 0.0) - u * t @ v).abs().max() < 1e-9
+        assert (ref.orthogonal(x, 5, 0.0, held=True) - u * t @ v).norm() < 0.05 * t.norm()
+
+
+def test_held_forms_stay_inside_binary16():
+    """Over the whole range of singular values: X below 2^6 * 1.21, S and its polynomial below 65504."""
+    a, b, c = ref.QUINTIC
+    s = torch.linspace(0, 1.21, 100_001, dtype=torch.float64)
+    assert (a * s + b * s ** 3 + c * s ** 5).abs().max() < 1.21
+    assert s.square().max() * ref.HELD[1] < 65504 / 2 and (b * s ** 2 + c * s ** 4).abs().max() * ref.HELD[2] < 65504 / 2
+
+
+def test_orthogonalize_refusals(L):
+    g, out, ws = BASE, BASE + 64 * MB, BASE + 128 * MB
+    need = L.ring_orthogonalize_workspace(3, 100, 200)
+    assert need > 3 * 2 * 128 * 256 * 2 and L.ring_orthogonalize_workspace(0, 5, 5) == 0
+    assert L.ring_orthogonalize_workspace(65536, 5, 5) == 0
+
+    def call(g=g, ldg=200, sg=20000, dt=F32, out=out, ldo=200, so=20000, odt=BF16, batch=3, rows=100, cols=200, steps=5, eps=1e-7,
+             ws=ws, wb=need):
+        return L.ring_orthogonalize(g, ldg, sg, dt, out, ldo, so, odt, batch, rows, cols, steps, eps, ws, wb, None)
+
+    assert call() == ECUDA and call(out=g, odt=F32) == ECUDA and call(batch=1, sg=0, so=0) == ECUDA
+    assert call(batch=0) == OK and call(rows=0) == OK and call(cols=0) == OK
+    assert call(dt=3) == EINVAL and call(odt=-1) == EINVAL and call(steps=0) == EINVAL and call(steps=1001) == EINVAL
+    assert call(eps=-1e-9) == EINVAL and call(eps=float("nan")) == EINVAL and call(eps=float("inf")) == EINVAL
+    assert call(g=None) == EINVAL and call(g=g + 2) == EINVAL and call(out=out + 1) == EINVAL and call(ldg=199) == EINVAL
+    assert call(ldo=199) == EINVAL and call(sg=19999) == EINVAL and call(so=19999) == EINVAL and call(batch=65536) == EINVAL
+    assert call(rows=1 << 31) == EINVAL and call(wb=need - 1) == EINVAL and call(ws=None) == EINVAL and call(ws=ws + 16) == EINVAL
+    assert call(out=g) == EALIAS and call(out=g + 400) == EALIAS and call(ws=g) == EALIAS and call(ws=out) == EALIAS
+    assert call(out=g, odt=F32, ldo=201, so=30000) == EALIAS

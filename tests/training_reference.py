@@ -45,3 +45,26 @@ def cross_entropy_grad(grad, l, target, ignore_index):
     e = torch.softmax(l, 1)
     e[torch.arange(l.shape[0], device=l.device), torch.where(counts, target, 0)] -= 1
     return e * (torch.where(counts, 1.0, 0.0) * grad.double())[:, None]
+
+
+QUINTIC = (3.4445, -4.7750, 2.0315)
+HELD = (2.0 ** 6, 2.0 ** 14, 2.0 ** 13)  # what X, S and b S + c S^2 are held times
+
+
+def orthogonal(g, steps, eps, held=False):
+    """Newton-Schulz steps in 64 bits; held: with X, S and the polynomial rounded to binary16 as the kernels hold them."""
+    def keep(t, scale):
+        return (t * scale).half().double() / scale if held else t
+
+    x = g.double()
+    tall = x.shape[-2] > x.shape[-1]
+    x = x.mT if tall else x
+    x = keep(x / (torch.linalg.matrix_norm(x).unsqueeze(-1).unsqueeze(-1) + eps), HELD[0])
+    a, b, c = QUINTIC
+    for k in range(steps):
+        s = keep(x @ x.mT, HELD[1])
+        p = keep(b * s + c * (s @ s), HELD[2])
+        x = a * x + p @ x
+        if k + 1 < steps:
+            x = keep(x, HELD[0])
+    return x.mT if tall else x

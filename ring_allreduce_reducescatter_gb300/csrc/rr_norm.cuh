@@ -63,6 +63,14 @@ __device__ __forceinline__ void widen(const Raw<DT, kN> &r, float v[kN]) {
     widen8<DT>(&u, v);
   }
 }
+// 16 bytes from shared memory.
+template <int DT>
+__device__ __forceinline__ void widen_shared(const unsigned char *from, float v[16 / Fmt<DT>::bytes]) {
+  const uint4 u = *reinterpret_cast<const uint4 *>(from);
+  Raw<DT, 16 / Fmt<DT>::bytes> r;
+  r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+  widen<DT, 16 / Fmt<DT>::bytes>(r, v);
+}
 template <int DT, int kN>
 __device__ __forceinline__ void store(void *base, long long at, const float v[kN]) {
   using T = typename Fmt<DT>::type;
@@ -235,21 +243,196 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
 // backward
 // --------------------------------------------------------------------------
 
+// A row on kRow threads, two groups of 16 bytes each; 256 threads or a row's a CTA.
+template <int kRow>
+constexpr int kRingThreads = kRow < 256 ? 256 : kRow;
+// Rows of x and dy wait in a ring of shared memory: a stage is the rows that a CTA
+// takes at once.
+template <int kRow>
+struct Ring {
+  static constexpr int kThreads = kRingThreads<kRow>, kRows = kThreads / kRow, kNv = 2;
+  static constexpr int kRowBytes = kRow * kNv * 16;      // at most
+  static constexpr int kHalf = kRows * kRowBytes;        // x, or dy
+  static constexpr int kStages = kRow <= 256 ? 4 : 3;
+  static constexpr int kCtas = kThreads == 256 ? 3 : kThreads == 512 ? 2 : 1;  // an SM
+  static constexpr int kSmem = kStages * 2 * kHalf;
+};
+
+// Sums of two values over kRow threads, to all of them.  slots: this turn's; the
+// barrier in here also ends the CTA's reads of the turn before.
+template <int kRow>
+__device__ __forceinline__ void row_sums(float &a, float &b, float (*slots)[32]) {
+#pragma unroll
+  for (int d = kRow < 32 ? kRow / 2 : 16; d > 0; d /= 2)
+    a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, d)), b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, d));
+  constexpr int kWarps = kRow / 32;
+  if constexpr (kWarps > 1) {
+    const int warp = threadIdx.x / 32, from = warp / kWarps * kWarps;
+    if (threadIdx.x % 32 == 0) slots[0][warp] = a, slots[1][warp] = b;
+    __syncthreads();
+    if constexpr (kWarps == 2) {
+      a = __fadd_rn(slots[0][from], slots[0][from + 1]), b = __fadd_rn(slots[1][from], slots[1][from + 1]);
+    } else {
+      a = b = 0.f;
+#pragma unroll
+      for (int j = 0; j < kWarps; j += 4) {
+        const float4 u = *reinterpret_cast<const float4 *>(&slots[0][from + j]), v = *reinterpret_cast<const float4 *>(&slots[1][from + j]);
+        a = __fadd_rn(a, __fadd_rn(__fadd_rn(u.x, u.y), __fadd_rn(u.z, u.w)));
+        b = __fadd_rn(b, __fadd_rn(__fadd_rn(v.x, v.y), __fadd_rn(v.z, v.w)));
+      }
+    }
+  } else {
+    __syncthreads();
+  }
+}
+
+// Rows whose 16-byte groups are aligned.  Persistent CTAs walk the rows; bulk
+// copies bring the next ones into the ring while these are finished, so what is in
+// flight does not depend on registers (holding it there left 16384 x 4096 bfloat16
+// at 132 us of the 59 that memory takes).  A thread keeps its columns throughout,
+// and with them their part of dweight and dbias in registers: the sums over rows
+// cost one write of two rows a CTA, and the rest is norm_sums_kernel's.  Rows go to
+// CTAs by their index, so the order of the sums does not depend on timing.
+template <int DT, int WT, int kRow>
+__global__ void __launch_bounds__(Ring<kRow>::kThreads, Ring<kRow>::kCtas)
+    norm_grad_ring_kernel(const __grid_constant__ NormGradParams p) {
+  using R = Ring<kRow>;
+  using T = typename Fmt<DT>::type;
+  constexpr int kW = kWide<DT, true>, kNv = R::kNv;
+  extern __shared__ __align__(128) unsigned char ring[];
+  __shared__ __align__(16) float slots[2][2][32];
+  __shared__ __align__(8) uint64_t full[R::kStages];
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < R::kStages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const int t = threadIdx.x % kRow, group = threadIdx.x / kRow;
+  const int cols = (int)p.cols, row_bytes = cols * (int)sizeof(T);
+  const float inv = __fdiv_rn(1.f, (float)cols);
+  float dw[kNv][kW], db[kNv][kW];
+#pragma unroll
+  for (int k = 0; k < kNv; ++k)
+#pragma unroll
+    for (int j = 0; j < kW; ++j) dw[k][j] = db[k][j] = 0.f;
+  const long long step = (long long)gridDim.x * R::kRows, start = (long long)blockIdx.x * R::kRows;
+  const unsigned turns = start < p.rows ? (unsigned)((p.rows - start + step - 1) / step) : 0;
+  // turn q's rows into its stage, by thread 0
+  auto fetch = [&](unsigned q) {
+    const long long first = start + q * step;
+    const int n = (int)(p.rows - first < R::kRows ? p.rows - first : R::kRows);
+    const unsigned s = q % R::kStages;
+    const uint64_t pol = l2_evict_first_policy();
+    unsigned char *to = ring + s * 2 * R::kHalf;
+    mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * n * row_bytes));
+    for (int r = 0; r < n; ++r) {
+      bulk_load(to + r * R::kRowBytes, static_cast<const T *>(p.x) + (first + r) * p.ld_x, row_bytes, &full[s], pol);
+      bulk_load(to + R::kHalf + r * R::kRowBytes, static_cast<const T *>(p.dy) + (first + r) * p.ld_dy, row_bytes, &full[s], pol);
+    }
+  };
+  if (threadIdx.x == 0)
+    for (unsigned q = 0; q + 1 < R::kStages && q < turns; ++q) fetch(q);
+  long long row = start + group;
+  float mean = 0.f, rstd = 0.f;
+  if (row < p.rows) mean = p.mean[row], rstd = p.rstd[row];
+  bool ok = true;
+  for (unsigned q = 0; q < turns; ++q, row += step) {
+    const bool live = row < p.rows;
+    const float shift = mean, scale = live ? rstd : 0.f;
+    if (row + step < p.rows) mean = p.mean[row + step], rstd = p.rstd[row + step];
+    const unsigned s = q % R::kStages;
+    // (a wait that gave up: every thread still comes to every barrier, and stores nothing more)
+    ok = mbar_wait_bounded(&full[s], (q / R::kStages) & 1, ok ? kWaitLimitNs : 0) && ok;
+    const unsigned char *from = ring + s * 2 * R::kHalf + group * R::kRowBytes + t * 16;
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+      const int c = (t + k * kRow) * kW;
+      if (c >= cols || !live) continue;
+      float x[kW], d[kW], w[kW];
+      widen_shared<DT>(from + k * kRow * 16, x);
+      widen_shared<DT>(from + R::kHalf + k * kRow * 16, d);
+      load_weight<WT, kW>(p.weight, c, 1.f, w);
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        const float h = __fmul_rn(__fsub_rn(x[j], shift), scale), g = __fmul_rn(d[j], w[j]);
+        dw[k][j] = __fmaf_rn(d[j], h, dw[k][j]);
+        db[k][j] = __fadd_rn(db[k][j], d[j]);
+        s1 = __fadd_rn(s1, g);
+        s2 = __fmaf_rn(g, h, s2);
+      }
+    }
+    row_sums<kRow>(s1, s2, slots[q & 1]);
+    // every thread is past the turn before: its stage is free
+    if (threadIdx.x == 0 && q + R::kStages - 1 < turns) fetch(q + R::kStages - 1);
+    if (!p.dx || !live || !ok) continue;
+    s1 = __fmul_rn(s1, inv), s2 = __fmul_rn(s2, inv);
+#pragma unroll
+    for (int k = 0; k < kNv; ++k) {
+      const int c = (t + k * kRow) * kW;
+      if (c >= cols) continue;
+      float x[kW], d[kW], w[kW];
+      widen_shared<DT>(from + k * kRow * 16, x);
+      widen_shared<DT>(from + R::kHalf + k * kRow * 16, d);
+      load_weight<WT, kW>(p.weight, c, 1.f, w);
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        const float h = __fmul_rn(__fsub_rn(x[j], shift), scale);
+        d[j] = __fmul_rn(__fsub_rn(__fmaf_rn(-h, s2, __fmul_rn(d[j], w[j])), s1), scale);
+      }
+      store<DT, kW>(p.dx, row * p.ld_dx + c, d);
+    }
+  }
+  if (!ok) {
+    // what is in flight lands before shared memory is given back
+    if (threadIdx.x % 32 == 0) atomicOr(p.status, kStatusWaitTimeout);
+    for (unsigned u = turns > R::kStages ? turns - R::kStages : 0; u < turns; ++u)
+      mbar_wait_bounded(&full[u % R::kStages], (u / R::kStages) & 1, kWaitLimitNs);
+  }
+  if (!p.sums) return;
+  float *out = p.partials + (long long)blockIdx.x * 2 * p.cols;
+  float *sums = reinterpret_cast<float *>(ring);
+#pragma unroll
+  for (int half = 0; half < 2; ++half, out += p.cols) {
+    if constexpr (R::kRows > 1) {
+      // the groups' sums in their order
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kNv; ++k)
+#pragma unroll
+        for (int j = 0; j < kW; ++j) sums[group * (kRow * kNv * kW) + (t + k * kRow) * kW + j] = half ? db[k][j] : dw[k][j];
+      __syncthreads();
+      for (int c = threadIdx.x; c < cols; c += R::kThreads) {
+        float v = sums[c];
+        for (int g = 1; g < R::kRows; ++g) v = __fadd_rn(v, sums[g * (kRow * kNv * kW) + c]);
+        out[c] = v;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kNv; ++k) {
+        const int c = (t + k * kRow) * kW;
+        if (c >= cols) continue;
+#pragma unroll
+        for (int j = 0; j < kW; j += 4) {
+          const float *v = half ? &db[k][j] : &dw[k][j];
+          *reinterpret_cast<float4 *>(out + c + j) = make_float4(v[0], v[1], v[2], v[3]);
+        }
+      }
+    }
+  }
+}
+
 template <int kRow>
 constexpr int kGradThreads = kRow < 256 ? 256 : kRow;
 
-// Persistent CTAs walk the rows, the next row's x and dy on their way while this
-// one is finished.  A thread keeps its columns throughout, and with them their
-// part of dweight and dbias in registers: the sums over rows cost one write of
-// two rows a CTA, and the rest is norm_sums_kernel's.  x and dy stay in storage
-// format between the sums and dx, and weight comes from L1 both times: 1024
-// threads an SM leave 64 registers each.  Rows go to CTAs by their index, so the
-// order of the sums does not depend on timing.
-template <int DT, int WT, bool kVec, int kRow, int kNv>
+// The same by single elements, for rows that are not aligned: x and dy stay in
+// storage format between the sums and dx, and weight comes from L1 both times.
+template <int DT, int WT, int kRow, int kNv>
 __global__ void __launch_bounds__(kGradThreads<kRow>, kGradThreads<kRow> <= 512 ? 1024 / kGradThreads<kRow> : 1)
     norm_grad_kernel(const __grid_constant__ NormGradParams p) {
-  constexpr int kW = kWide<DT, kVec>, kCta = kGradThreads<kRow>, kRows = kCta / kRow;
-  constexpr bool kAhead = kVec;  // (by single elements the registers go to this row's)
+  constexpr int kW = 1, kCta = kGradThreads<kRow>, kRows = kCta / kRow;
   __shared__ float slots[2][2][32];
   __shared__ float sums[kRows > 1 ? kCta * kNv * kW : 1];
   grid_dependency_wait();
@@ -280,10 +463,9 @@ __global__ void __launch_bounds__(kGradThreads<kRow>, kGradThreads<kRow> <= 512 
     }
   };
   long long row = (long long)blockIdx.x * kRows + group;
-  if (kAhead) fetch(row);
   int turn = 0;
   for (long long first = (long long)blockIdx.x * kRows; first < p.rows; first += step, row += step, turn ^= 1) {
-    if (!kAhead) fetch(row);
+    fetch(row);
     Raw<DT, kW> cx[kNv], cd[kNv];
     const float scale = rstd, shift = mean;
     float s1 = 0.f, s2 = 0.f;
@@ -305,7 +487,6 @@ __global__ void __launch_bounds__(kGradThreads<kRow>, kGradThreads<kRow> <= 512 
         s2 = __fmaf_rn(g, h, s2);
       }
     }
-    if (kAhead) fetch(row + step);
     if (!p.dx) continue;
     s1 = warp_sum(s1), s2 = warp_sum(s2);
     if constexpr (kRow > 32) {
@@ -436,30 +617,45 @@ __global__ void __launch_bounds__(128) norm_columns_kernel(const __grid_constant
   for (int j = 0; j < kW; ++j) out[j] = dw[j], out[p.cols + j] = db[j];
 }
 
-// The partial sums of a column, in one order: eight threads a column take every
-// eighth one, and their sums are added up in turn.  blockIdx.y: dweight or dbias.
-template <int WT>
+// The partial sums of a column, in one order: sixteen threads a column take every
+// sixteenth one, and their sums are added up in turn.  A thread takes kC columns
+// (four where a row of the partial sums is whole groups of 16 bytes); blockIdx.y:
+// dweight or dbias.
+template <int WT, int kC>
 __global__ void __launch_bounds__(256) norm_sums_kernel(const float *partials, int parts, long long cols, void *dweight,
                                                         void *dbias) {
-  __shared__ float s[8][33];
+  __shared__ float s[16][16 * kC + 1];
   grid_dependency_wait();
   grid_dependents_launch();
   void *out = blockIdx.y ? dbias : dweight;
   if (!out) return;
-  const long long c = (long long)blockIdx.x * 32 + threadIdx.x;
-  float v = 0.f;
+  const long long c = ((long long)blockIdx.x * 16 + threadIdx.x) * kC;
+  float v[kC];
+#pragma unroll
+  for (int j = 0; j < kC; ++j) v[j] = 0.f;
   if (c < cols) {
     const float *from = partials + blockIdx.y * cols + c;
 #pragma unroll 8
-    for (int q = threadIdx.y; q < parts; q += 8) v = __fadd_rn(v, from[(long long)q * 2 * cols]);
+    for (int q = threadIdx.y; q < parts; q += 16) {
+      const float *at = from + (long long)q * 2 * cols;
+      if constexpr (kC == 4) {
+        const float4 u = *reinterpret_cast<const float4 *>(at);
+        v[0] = __fadd_rn(v[0], u.x), v[1] = __fadd_rn(v[1], u.y), v[2] = __fadd_rn(v[2], u.z), v[3] = __fadd_rn(v[3], u.w);
+      } else {
+        v[0] = __fadd_rn(v[0], *at);
+      }
+    }
   }
-  s[threadIdx.y][threadIdx.x] = v;
-  __syncthreads();
-  if (threadIdx.y == 0 && c < cols) {
 #pragma unroll
-    for (int j = 1; j < 8; ++j) v = __fadd_rn(v, s[j][threadIdx.x]);
-    static_cast<typename Fmt<WT>::type *>(out)[c] = from_f32<WT>(v);
-  }
+  for (int j = 0; j < kC; ++j) s[threadIdx.y][threadIdx.x * kC + j] = v[j];
+  __syncthreads();
+  const int tid = threadIdx.y * 16 + threadIdx.x;
+  const long long at = (long long)blockIdx.x * 16 * kC + tid;
+  if (tid >= 16 * kC || at >= cols) return;
+  float total = s[0][tid];
+#pragma unroll
+  for (int j = 1; j < 16; ++j) total = __fadd_rn(total, s[j][tid]);
+  static_cast<typename Fmt<WT>::type *>(out)[at] = from_f32<WT>(total);
 }
 
 // --------------------------------------------------------------------------
@@ -467,10 +663,11 @@ __global__ void __launch_bounds__(256) norm_sums_kernel(const float *partials, i
 // --------------------------------------------------------------------------
 
 template <class... P, class... Args>
-cudaError_t launch(void (*k)(P...), dim3 grid, dim3 block, cudaStream_t s, const Args &...args) {
+cudaError_t launch_smem(void (*k)(P...), dim3 grid, dim3 block, int smem, cudaStream_t s, const Args &...args) {
   cudaLaunchConfig_t c = {};
   c.gridDim = grid;
   c.blockDim = block;
+  c.dynamicSmemBytes = smem;
   c.stream = s;
   cudaLaunchAttribute a = {};
   a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -478,6 +675,11 @@ cudaError_t launch(void (*k)(P...), dim3 grid, dim3 block, cudaStream_t s, const
   c.attrs = &a;
   c.numAttrs = 1;
   return cudaLaunchKernelEx(&c, k, args...);
+}
+
+template <class... P, class... Args>
+cudaError_t launch(void (*k)(P...), dim3 grid, dim3 block, cudaStream_t s, const Args &...args) {
+  return launch_smem(k, grid, block, 0, s, args...);
 }
 
 template <int DT, int WT, bool kVec, int kRow, int kNv>
@@ -503,27 +705,42 @@ cudaError_t forward(const NormParams &p, cudaStream_t s) {
     return launch(norm_long_kernel<DT, WT, true>, dim3((unsigned)p.rows), dim3(1024), s, p);
   }
   if (p.cols <= 256) return forward_of<DT, WT, false, 32, 8>(p, s);
+  if (p.cols <= 512) return forward_of<DT, WT, false, 64, 8>(p, s);
   if (p.cols <= 1024) return forward_of<DT, WT, false, 128, 8>(p, s);
   if (p.cols <= 2048) return forward_of<DT, WT, false, 256, 8>(p, s);
   if (p.cols <= 4096) return forward_of<DT, WT, false, 512, 8>(p, s);
+  if (p.cols <= 8192) return forward_of<DT, WT, false, 1024, 8>(p, s);
   if (p.cols <= 16384) return forward_of<DT, WT, false, 1024, 16>(p, s);
   return launch(norm_long_kernel<DT, WT, false>, dim3((unsigned)p.rows), dim3(1024), s, p);
 }
 
 template <int WT>
 cudaError_t finish_sums(const NormGradParams &p, int parts, cudaStream_t s) {
-  return launch(norm_sums_kernel<WT>, dim3((unsigned)ceil_div(p.cols, 32ll), 2), dim3(32, 8), s,
-                (const float *)p.partials, parts, p.cols, p.dweight, p.dbias);
+  return p.cols % 4 == 0 ? launch(norm_sums_kernel<WT, 4>, dim3((unsigned)ceil_div(p.cols, 64ll), 2), dim3(16, 16), s,
+                                  (const float *)p.partials, parts, p.cols, p.dweight, p.dbias)
+                         : launch(norm_sums_kernel<WT, 1>, dim3((unsigned)ceil_div(p.cols, 16ll), 2), dim3(16, 16), s,
+                                  (const float *)p.partials, parts, p.cols, p.dweight, p.dbias);
 }
-template <int DT, int WT, bool kVec, int kRow, int kNv>
-cudaError_t backward_of(const NormGradParams &p, cudaStream_t s) {
-  constexpr int kCta = kGradThreads<kRow>, kRows = kCta / kRow;
-  const long long fit = (long long)p.sms * (kCta <= 512 ? 1024 / kCta : 1);
-  long long grid = ceil_div(p.rows, (long long)kRows);
-  if (grid > fit) grid = fit;
+// One launch over the rows and, where they are wanted, one for the sums.
+template <int WT, class K>
+cudaError_t backward_by(K kernel, int rows_a_cta, int threads, int ctas, int smem, const NormGradParams &p, cudaStream_t s) {
+  long long grid = ceil_div(p.rows, (long long)rows_a_cta);
+  if (grid > (long long)p.sms * ctas) grid = (long long)p.sms * ctas;
   if (grid > p.parts) grid = p.parts;
-  const cudaError_t e = launch(norm_grad_kernel<DT, WT, kVec, kRow, kNv>, dim3((unsigned)grid), dim3(kCta), s, p);
+  const cudaError_t e = launch_smem(kernel, dim3((unsigned)grid), dim3((unsigned)threads), smem, s, p);
   return e != cudaSuccess || !p.sums ? e : finish_sums<WT>(p, (int)grid, s);
+}
+template <int DT, int WT, int kRow, int kNv>
+cudaError_t backward_of(const NormGradParams &p, cudaStream_t s) {
+  constexpr int kCta = kGradThreads<kRow>;
+  return backward_by<WT>(norm_grad_kernel<DT, WT, kRow, kNv>, kCta / kRow, kCta, kCta <= 512 ? 1024 / kCta : 1, 0, p, s);
+}
+template <int DT, int WT, int kRow>
+cudaError_t backward_ring(const NormGradParams &p, cudaStream_t s) {
+  using R = Ring<kRow>;
+  const cudaError_t e = allow_smem<norm_grad_ring_kernel<DT, WT, kRow>>(R::kSmem);
+  if (e != cudaSuccess) return e;
+  return backward_by<WT>(norm_grad_ring_kernel<DT, WT, kRow>, R::kRows, R::kThreads, R::kCtas, R::kSmem, p, s);
 }
 template <int DT, int WT, bool kVec>
 cudaError_t backward_long(const NormGradParams &p, cudaStream_t s) {
@@ -541,20 +758,20 @@ cudaError_t backward(const NormGradParams &p, cudaStream_t s) {
   if (p.rows == 0) return p.sums ? finish_sums<WT>(p, 0, s) : cudaSuccess;
   if (p.vec) {
     const long long g = p.cols / kWide<DT, true>;
-    if (g <= 32) return backward_of<DT, WT, true, 32, 1>(p, s);
-    if (g <= 64) return backward_of<DT, WT, true, 32, 2>(p, s);
-    if (g <= 128) return backward_of<DT, WT, true, 128, 1>(p, s);
-    if (g <= 256) return backward_of<DT, WT, true, 256, 1>(p, s);
-    if (g <= 512) return backward_of<DT, WT, true, 512, 1>(p, s);
-    if (g <= 1024) return backward_of<DT, WT, true, 512, 2>(p, s);
-    if (g <= 2048 && p.cols <= kNormLongRow) return backward_of<DT, WT, true, 1024, 2>(p, s);
+    if (g <= 32) return backward_ring<DT, WT, 16>(p, s);
+    if (g <= 64) return backward_ring<DT, WT, 32>(p, s);
+    if (g <= 128) return backward_ring<DT, WT, 64>(p, s);
+    if (g <= 256) return backward_ring<DT, WT, 128>(p, s);
+    if (g <= 512) return backward_ring<DT, WT, 256>(p, s);
+    if (g <= 1024) return backward_ring<DT, WT, 512>(p, s);
+    if (g <= 2048) return backward_ring<DT, WT, 1024>(p, s);
     return backward_long<DT, WT, true>(p, s);
   }
-  if (p.cols <= 256) return backward_of<DT, WT, false, 32, 8>(p, s);
-  if (p.cols <= 1024) return backward_of<DT, WT, false, 128, 8>(p, s);
-  if (p.cols <= 2048) return backward_of<DT, WT, false, 256, 8>(p, s);
-  if (p.cols <= 4096) return backward_of<DT, WT, false, 512, 8>(p, s);
-  if (p.cols <= 8192) return backward_of<DT, WT, false, 1024, 8>(p, s);
+  if (p.cols <= 256) return backward_of<DT, WT, 32, 8>(p, s);
+  if (p.cols <= 1024) return backward_of<DT, WT, 128, 8>(p, s);
+  if (p.cols <= 2048) return backward_of<DT, WT, 256, 8>(p, s);
+  if (p.cols <= 4096) return backward_of<DT, WT, 512, 8>(p, s);
+  if (p.cols <= 8192) return backward_of<DT, WT, 1024, 8>(p, s);
   return backward_long<DT, WT, false>(p, s);
 }
 

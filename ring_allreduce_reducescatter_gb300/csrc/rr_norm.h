@@ -26,14 +26,15 @@ struct NormGradParams {
   float *partials;             // [parts][2][cols]: sums over some rows of dy h and of dy (null with no rows)
   long long rows, cols, ld_dy, ld_x, ld_dx;
   int parts, dtype, wtype, sms;
+  unsigned int *status;
   bool sums;  // dweight or dbias is wanted
   bool vec;
 };
 
 // The most partial sums of the weights' gradients that a backward pass keeps:
-// two CTAs an SM of 152 where a CTA holds whole rows, and few where rows are
-// longer than its registers and memory would go to the partial sums.
-constexpr long long kNormParts = 304, kNormLongParts = 64, kNormLongRow = 8192;
+// three CTAs an SM of 152 where a CTA holds whole rows, and few where rows are
+// long and memory would go to the partial sums.
+constexpr long long kNormParts = 456, kNormLongParts = 152, kNormLongRow = 8192;
 inline long long norm_parts(long long rows, long long cols) {
   const long long most = cols <= kNormLongRow ? kNormParts : kNormLongParts;
   return rows < most ? rows : most;

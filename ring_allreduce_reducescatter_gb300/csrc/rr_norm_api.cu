@@ -99,8 +99,7 @@ rr_status ring_layer_norm_backward(const void *dy, size_t ld_dy, const void *x, 
   p.dtype = dtype, p.wtype = wtype;
   p.vec = cols * E % 16 == 0 && aligned16(dy, rows, ld_dy, E) && aligned16(x, rows, ld_x, E) &&
           (!dx || aligned16(dx, rows, ld_dx, E)) && vec16(weight);
-  unsigned *status;
-  const rr_status st = rr::device_info(&status, &p.sms);
+  const rr_status st = rr::device_info(&p.status, &p.sms);
   if (st != RR_OK) return st;
   return launched(dtype == RR_FP32   ? rr::launch_norm_grad_f32(p, stream)
                   : dtype == RR_FP16 ? rr::launch_norm_grad_f16(p, stream)

@@ -16,6 +16,7 @@ struct NormParams {
   long long rows, cols, ld_x, ld_out;
   float eps;
   int dtype, wtype, sms;
+  unsigned int *status;
   bool vec;  // 16-byte groups of the rows of x and out, and of weight and bias, are aligned; cols is whole groups
 };
 
@@ -32,11 +33,11 @@ struct NormGradParams {
 };
 
 // The most partial sums of the weights' gradients that a backward pass keeps:
-// three CTAs an SM of 152 where a CTA holds whole rows, and few where rows are
+// three CTAs an SM of 152 where a CTA holds whole rows, and fewer where rows are
 // long and memory would go to the partial sums.
-constexpr long long kNormParts = 456, kNormLongParts = 152, kNormLongRow = 8192;
+constexpr long long kNormParts = 456, kNormLongParts = 304, kNormLongRow = 4096, kNormOverRow = 16384, kNormOverParts = 32;
 inline long long norm_parts(long long rows, long long cols) {
-  const long long most = cols <= kNormLongRow ? kNormParts : kNormLongParts;
+  const long long most = cols <= kNormLongRow ? kNormParts : cols <= kNormOverRow ? kNormLongParts : kNormOverParts;
   return rows < most ? rows : most;
 }
 

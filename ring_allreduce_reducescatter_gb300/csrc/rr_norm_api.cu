@@ -60,6 +60,8 @@ rr_status ring_layer_norm(const void *x, size_t ld_x, const void *weight, const 
   p.eps = (float)eps;
   p.dtype = dtype, p.wtype = wtype;
   p.vec = cols * E % 16 == 0 && aligned16(x, rows, ld_x, E) && aligned16(out, rows, ld_out, E) && vec16(weight) && vec16(bias);
+  const rr_status st = rr::device_info(&p.status, &p.sms);
+  if (st != RR_OK) return st;
   return launched(dtype == RR_FP32   ? rr::launch_norm_f32(p, stream)
                   : dtype == RR_FP16 ? rr::launch_norm_f16(p, stream)
                                      : rr::launch_norm_bf16(p, stream));

@@ -306,6 +306,167 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
   if (warp == 9) tmem_free<G>(tmem, S::kColumns);
 }
 
+// --------------------------------------------------------------------------
+// few tiles: K split over a cluster
+// --------------------------------------------------------------------------
+
+// A cluster of S CTAs (2, 4 or 8) computes one tile of 128 x 128, each CTA a
+// contiguous part of K.  Each sends its sums, 32 columns (64 for two CTAs) to each
+// of up to four owners, to a place of its own in the owner's shared memory; one
+// barrier later the owners add up what they received, in rank order (the result
+// does not depend on timing), and finish it.  A grid of whole tiles would leave most
+// SMs without a share of the work: 33 x 1024 by K of 8000 took 30 us whole.
+struct Split {
+  static constexpr int kStages = 3, kStageBytes = 2 * 128 * 128;
+  static constexpr int kThreads = 320;  // warps 0-7 epilogue, 8 copies, 9 products
+  static constexpr uint32_t kColumns = 128;
+  static __host__ __device__ constexpr int owners(int split) { return split < 4 ? split : 4; }
+  static __host__ __device__ constexpr int part_bytes(int split) { return 128 * 128 * 4 / owners(split); }
+  static __host__ __device__ constexpr int smem(int split) { return 1024 + kStages * kStageBytes + split * part_bytes(split); }
+  static_assert(kStages * kStageBytes >= 8 * kStageFloats * 4, "the ragged epilogue fits the stages");
+};
+
+template <bool kMnA, bool kMnB, class Epi>
+__global__ void __launch_bounds__(Split::kThreads, 1)
+    product_split_kernel(const __grid_constant__ Product p, const __grid_constant__ typename Epi::Params e, int split) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[Split::kStages], empty[Split::kStages], done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int failed;
+  unsigned char *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Split::kStages; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+    mbar_init(&done, 1);
+    failed = 0;
+    fence_mbar_init();
+  }
+  cluster_arrive();  // waited for before the first remote store: by then every CTA runs
+  if (warp == 9) tmem_alloc<1>(&tmem_slot, Split::kColumns);
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  const uint32_t tmem = (uint32_t)uniform((int)tmem_slot);
+  const int rank = blockIdx.x % split;
+  const Place w = place_of(p, blockIdx.x / split);
+  const int k0 = (int)((long long)p.steps * rank / split), n_steps = (int)((long long)p.steps * (rank + 1) / split) - k0;
+  grid_dependency_wait();
+  grid_dependents_launch();
+
+  if (warp == 8) {
+    const uint64_t pol = l2_evict_normal_policy();
+    const bool one = elect_one();
+    int k = 0;
+    for (; k < n_steps; ++k) {
+      const int s = k % Split::kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((k / Split::kStages) & 1) ^ 1, kWaitLimitNs))) break;
+      unsigned char *a = smem + s * Split::kStageBytes, *b = a + 128 * 128;
+      if (one) {
+        mbar_arrive_expect_tx(&full[s], Split::kStageBytes);
+        if constexpr (kMnA) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) load_box<1>(a + 8192 * j, &p.a, w.tm * 128 + 64 * j, (k0 + k) * kStep, w.batch, &full[s], 0, pol);
+        } else {
+          load_box<1>(a, &p.a, (k0 + k) * kStep, w.tm * 128, w.batch, &full[s], 0, pol);
+        }
+        if constexpr (kMnB) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) load_box<1>(b + 8192 * j, &p.b, w.tn * 128 + 64 * j, (k0 + k) * kStep, w.batch, &full[s], 0, pol);
+        } else {
+          load_box<1>(b, &p.b, (k0 + k) * kStep, w.tn * 128, w.batch, &full[s], 0, pol);
+        }
+      }
+      __syncwarp();
+    }
+    if (k < n_steps && one) {
+      atomicOr(p.status, kStatusWaitTimeout);
+      atomicExch(&failed, 1);
+    }
+    // the copies in flight land before shared memory is given back
+    wait_turns<Split::kStages>(full, k, kWaitLimitNs);
+  } else if (warp == 9) {
+    const bool one = elect_one();
+    const uint32_t idesc = instr_desc(p.format, kMnA, kMnB, 128, 128);
+    int k = 0;
+    for (; k < n_steps; ++k) {
+      const int s = k % Split::kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (k / Split::kStages) & 1, kWaitLimitNs))) break;
+      tcgen05_fence_after();
+      const uint32_t a = smem_addr(smem) + s * Split::kStageBytes, b = a + 128 * 128;
+      if (one) {
+#pragma unroll
+        for (int j = 0; j < kStep / 16; ++j)
+          mma<1>(tmem, kMnA ? rows_desc(a + 2048 * j) : operand_desc(a + 32 * j),
+                 kMnB ? rows_desc(b + 2048 * j) : operand_desc(b + 32 * j), idesc, k > 0 || j > 0);
+        tcgen05_commit<1>(&empty[s]);
+      }
+      __syncwarp();
+    }
+    if (one) {
+      if (k < n_steps) {
+        atomicOr(p.status, kStatusWaitTimeout);
+        atomicExch(&failed, 1);
+      }
+      tcgen05_commit<1>(&done);
+    }
+  }
+  __syncwarp();
+  // every warp waits here for the last product, so none leaves tensor memory or
+  // shared memory while they are in use
+  if (!mbar_wait_bounded(&done, 0, 2 * kWaitLimitNs) && lane == 0) {
+    atomicOr(p.status, kStatusWaitTimeout);
+    atomicExch(&failed, 1);
+  }
+  __syncwarp();
+  tcgen05_fence_after();
+  __syncthreads();
+
+  const int quarter = warp % 4, half = warp / 4, row = quarter * 32 + lane, owners = Split::owners(split);
+  float *got = reinterpret_cast<float *>(smem + Split::kStages * Split::kStageBytes);
+  const int part = Split::part_bytes(split) / 4;  // floats: [columns / 4][128 rows][4]
+  cluster_wait();
+  if (warp < 8) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t acc[kChunk];
+      tmem_load32(tmem + ((uint32_t)(quarter * 32) << 16) + half * 64 + c * kChunk, acc);
+      tmem_loaded32(acc);
+      const int g = half * 2 + c, owner = owners == 4 ? g : g / 2, at = owners == 4 ? 0 : g % 2;
+      const uint32_t to = cluster_addr(got + rank * part + at * (kChunk * 128) + row * 4, owner);
+#pragma unroll
+      for (int j = 0; j < kChunk; j += 4) cluster_store4(to + j * 128 * 4, make_uint4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]));
+    }
+  } else if (warp == 8) {
+    // the commits of the last turns come before the CTA goes: later ones would
+    // meet another's barrier
+    wait_turns<Split::kStages>(empty, n_steps, kLateLimitNs);
+  }
+  tcgen05_fence_before();
+  __syncthreads();
+  tcgen05_fence_after();
+  cluster_arrive();
+  if (warp == 9) tmem_free<1>(tmem, Split::kColumns);
+  cluster_wait();
+  if (rank < owners && half < 4 / owners && warp < 8 && !failed) {
+    const int first = rank * (128 / owners) + half * kChunk;
+    Epi epi(e, (long long)w.tm * 128 + row, (long long)w.tn * 128 + first, w.batch, reinterpret_cast<float *>(smem) + warp * kStageFloats);
+    float v[kChunk];
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) v[j] = 0.f;
+    for (int r = 0; r < split; ++r) {
+      const float4 *from = reinterpret_cast<const float4 *>(got + r * part + half * (kChunk * 128)) + row;
+#pragma unroll
+      for (int j = 0; j < kChunk; j += 4) {
+        const float4 x = from[j / 4 * 128];
+        v[j] = __fadd_rn(v[j], x.x), v[j + 1] = __fadd_rn(v[j + 1], x.y);
+        v[j + 2] = __fadd_rn(v[j + 2], x.z), v[j + 3] = __fadd_rn(v[j + 3], x.w);
+      }
+    }
+    epi.chunk(0, v);
+    epi.end();
+  }
+}
+
 template <bool kMnA, bool kMnB, class Epi>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_pair_kernel(const __grid_constant__ Product p, const __grid_constant__ typename Epi::Params e) {
@@ -387,17 +548,23 @@ constexpr long long kSmallOperand = 1 << 20;  // bytes
 // Defined in rr_gemm.cu: the map of an operand's boxes; `box` rows a box along K.
 bool make_operand_map(CUtensorMap *map, const Operand &o, int box);
 
+template <class S>
+bool fill_product(Product *q, const Operand &a, const Operand &b, bool upper, uint32_t format, unsigned int *status) {
+  q->m = a.rows, q->n = b.rows;
+  if (!make_operand_map(&q->a, a, 128) || !make_operand_map(&q->b, b, S::kRowsB)) return false;
+  q->steps = (int)ceil_div(a.k, (long long)kStep);
+  q->tiles_m = (int)ceil_div(q->m, (long long)S::kBM), q->tiles_n = (int)ceil_div(q->n, (long long)S::kBN);
+  q->per_batch = upper ? (long long)q->tiles_n * (q->tiles_n + 1) / 2 : (long long)q->tiles_m * q->tiles_n;
+  q->items = q->per_batch * b.batch;
+  q->format = format, q->upper = upper, q->status = status;
+  return true;
+}
+
 template <auto kKernel, class S, int G, class Params>
 cudaError_t launch_shape(const Operand &a, const Operand &b, bool upper, uint32_t format, unsigned int *status, int sms,
                          const Params &e, cudaStream_t s) {
   Product q;
-  q.m = a.rows, q.n = b.rows;
-  if (!make_operand_map(&q.a, a, 128) || !make_operand_map(&q.b, b, S::kRowsB)) return cudaErrorInvalidValue;
-  q.steps = (int)ceil_div(a.k, (long long)kStep);
-  q.tiles_m = (int)ceil_div(q.m, (long long)S::kBM), q.tiles_n = (int)ceil_div(q.n, (long long)S::kBN);
-  q.per_batch = upper ? (long long)q.tiles_n * (q.tiles_n + 1) / 2 : (long long)q.tiles_m * q.tiles_n;
-  q.items = q.per_batch * b.batch;
-  q.format = format, q.upper = upper, q.status = status;
+  if (!fill_product<S>(&q, a, b, upper, format, status)) return cudaErrorInvalidValue;
   const long long most = sms / G, workers = q.items < most ? q.items : most;
   const cudaError_t err = allow_smem<kKernel>(S::kSmem);
   if (err != cudaSuccess) return err;
@@ -414,13 +581,67 @@ cudaError_t launch_shape(const Operand &a, const Operand &b, bool upper, uint32_
   return cudaLaunchKernelEx(&c, kKernel, q, e);
 }
 
-// A product of a (its rows are D's rows) and b (D's columns).  upper: D is
-// symmetric, a and b the same matrix.  pair: the larger tiles.
+// CTAs a tile: none is split where the tiles fill the SMs, or K is short (an
+// exchange costs about 1.5 us, a step of K 0.15).
+inline int split_of(long long tiles, long long steps, int sms) {
+  if (tiles * 8 <= 64 && steps >= 32) return 8;
+  if (tiles * 4 <= sms && steps >= 12) return 4;
+  if (tiles * 2 <= sms && steps >= 16) return 2;
+  return 1;
+}
+
 template <bool kMnA, bool kMnB, class Epi>
-cudaError_t launch_product(const Operand &a, const Operand &b, bool upper, bool pair, uint32_t format, unsigned int *status,
-                           int sms, const typename Epi::Params &e, cudaStream_t s) {
-  return pair ? launch_shape<product_pair_kernel<kMnA, kMnB, Epi>, Pair, 2>(a, b, upper, format, status, sms, e, s)
-              : launch_shape<product_single_kernel<kMnA, kMnB, Epi>, Single, 1>(a, b, upper, format, status, sms, e, s);
+cudaError_t launch_split(const Operand &a, const Operand &b, bool upper, int split, uint32_t format, unsigned int *status,
+                         const typename Epi::Params &e, cudaStream_t s) {
+  Product q;
+  if (!fill_product<Single>(&q, a, b, upper, format, status)) return cudaErrorInvalidValue;
+  if (q.items * split > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+  const cudaError_t err = allow_smem<product_split_kernel<kMnA, kMnB, Epi>>(Split::smem(8));
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(q.items * split));
+  c.blockDim = dim3(Split::kThreads);
+  c.dynamicSmemBytes = Split::smem(split);
+  c.stream = s;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)split, at[1].val.clusterDim.y = 1, at[1].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = 2;
+  return cudaLaunchKernelEx(&c, product_split_kernel<kMnA, kMnB, Epi>, q, e, split);
+}
+
+// Which of the three a product takes.  The larger tiles once every pair of SMs has
+// one, or where the last turn of the smaller ones would cost more: a pair's turn
+// takes 1.5 times a single's.
+enum Kind { kSingle, kPair, kSplit };
+inline Kind kind_of(long long m, long long n, long long k, int batch, bool upper, int sms, int *split) {
+  const auto tiles = [&](long long side) {
+    const long long tm = ceil_div(m, side), tn = ceil_div(n, side);
+    return (upper ? tn * (tn + 1) / 2 : tm * tn) * batch;
+  };
+  const long long pairs = tiles(256), singles = tiles(128);
+  *split = split_of(singles, ceil_div(k, (long long)kStep), sms);
+  if (*split > 1) return kSplit;
+  return 3 * ceil_div(pairs, (long long)sms / 2) <= 2 * ceil_div(singles, (long long)sms) ? kPair : kSingle;
+}
+
+// A product of a (its rows are D's rows) and b (D's columns).  upper: D is
+// symmetric, a and b the same matrix.
+template <bool kMnA, bool kMnB, class Epi>
+cudaError_t launch_product(const Operand &a, const Operand &b, bool upper, uint32_t format, unsigned int *status, int sms,
+                           const typename Epi::Params &e, cudaStream_t s) {
+  int split;
+  switch (kind_of(a.rows, b.rows, a.k, b.batch, upper, sms, &split)) {
+    case kSplit:
+      return launch_split<kMnA, kMnB, Epi>(a, b, upper, split, format, status, e, s);
+    case kPair:
+      return launch_shape<product_pair_kernel<kMnA, kMnB, Epi>, Pair, 2>(a, b, upper, format, status, sms, e, s);
+    default:
+      return launch_shape<product_single_kernel<kMnA, kMnB, Epi>, Single, 1>(a, b, upper, format, status, sms, e, s);
+  }
 }
 
 }  // namespace gemm

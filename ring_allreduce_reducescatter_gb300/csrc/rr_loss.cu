@@ -182,16 +182,36 @@ __global__ void __launch_bounds__(1024) loss_factors_kernel(const __grid_constan
   if (threadIdx.x == 0) p.factors[tokens] = up;
 }
 
-// A copy in rows of ld_to, for operands that tensor copies do not read as they lie.
+// A copy in rows of ld_to, for operands that tensor copies do not read as they lie:
+// eight elements a thread, put together from the aligned 16-byte groups around them
+// where those lie inside the matrix.
 __global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ PadParams p) {
   grid_dependency_wait();
   grid_dependents_launch();
   const uint16_t *from = static_cast<const uint16_t *>(p.from);
   uint16_t *to = static_cast<uint16_t *>(p.to);
-  for (long long row = blockIdx.x; row < p.rows_to; row += gridDim.x) {
-    const long long cols = row < p.rows ? p.cols : 0;
-#pragma unroll 4
-    for (long long c = threadIdx.x; c < p.ld_to; c += 256) to[row * p.ld_to + c] = c < cols ? from[row * p.ld_from + c] : (uint16_t)0;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(from), hi = lo + (uintptr_t)(((p.rows - 1) * p.ld_from + p.cols) * 2);
+  const long long each = p.ld_to / 8, all = each * p.rows_to, step = gridDim.x * 256ll;
+#pragma unroll 2
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += step) {
+    const long long row = i < 0x7fffffff ? (long long)((unsigned)i / (unsigned)each) : i / each, c = (i - row * each) * 8;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < p.rows) {
+      const uint16_t *at = from + row * p.ld_from + c;
+      const uintptr_t a = reinterpret_cast<uintptr_t>(at), group = a & ~(uintptr_t)15;
+      if (c + 8 <= p.cols && group >= lo && group + 32 <= hi) {
+        v = funnel16(ldg_l1(reinterpret_cast<const void *>(group)), ldg_l1(reinterpret_cast<const void *>(group + 16)), (int)(a & 15));
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x = c + 2 * j < p.cols ? at[2 * j] : 0, y = c + 2 * j + 1 < p.cols ? at[2 * j + 1] : 0;
+          w[j] = x | y << 16;
+        }
+        v = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    *reinterpret_cast<uint4 *>(to + row * p.ld_to + c) = v;
   }
 }
 
@@ -212,7 +232,8 @@ cudaError_t launch(void (*k)(P...), long long grid, int block, cudaStream_t s, c
 }  // namespace
 
 cudaError_t launch_pad(const PadParams &p, cudaStream_t s) {
-  return launch(pad_kernel, p.rows_to < 8192 ? p.rows_to : 8192, 256, s, p);
+  const long long groups = ceil_div(p.rows_to * (p.ld_to / 8), 256ll);
+  return launch(pad_kernel, groups < 2048 ? groups : 2048, 256, s, p);
 }
 
 cudaError_t launch_loss(const LossParams &p, cudaStream_t s) {
@@ -220,8 +241,13 @@ cudaError_t launch_loss(const LossParams &p, cudaStream_t s) {
   if (tokens == 0) return launch(loss_sums_kernel, 1, 1024, s, p);
   const gemm::Operand a{p.x.at, p.x.padded, p.hidden, p.x.ld, 0, 1, false}, b{p.w.at, vocabulary, p.hidden, p.w.ld, 0, 1, false};
   const Statistics::Params e{p.target, p.parts, p.chosen, tokens, vocabulary, group};
-  cudaError_t err = gemm::launch_product<false, false, Statistics>(a, b, false, loss_pairs(tokens), p.dtype == kBF16, p.status,
-                                                                   p.sms, e, s);
+  // (groups of columns go by the tiles' width: the tokens alone choose)
+  const uint32_t format = p.dtype == kBF16;
+  cudaError_t err =
+      loss_pairs(tokens) ? gemm::launch_shape<gemm::product_pair_kernel<false, false, Statistics>, gemm::Pair, 2>(
+                               a, b, false, format, p.status, p.sms, e, s)
+                         : gemm::launch_shape<gemm::product_single_kernel<false, false, Statistics>, gemm::Single, 1>(
+                               a, b, false, format, p.status, p.sms, e, s);
   if (err != cudaSuccess) return err;
   // few rows: a CTA on each (one token of 131072 has 2048 groups)
   err = tokens <= 4 * p.sms ? launch(loss_rows_kernel<1>, tokens, 256, s, p, groups)

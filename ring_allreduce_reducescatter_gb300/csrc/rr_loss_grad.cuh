@@ -131,11 +131,6 @@ struct Summed {
 inline bool rows32(const void *p, long long ld, int bytes) {
   return reinterpret_cast<uintptr_t>(p) % 32 == 0 && ld * bytes % 32 == 0;
 }
-// The larger tiles once every pair of SMs has one.
-inline bool by_pairs(long long m, long long n, int sms) {
-  return ceil_div(m, (long long)gemm::Pair::kBM) * ceil_div(n, (long long)gemm::Pair::kBN) >= sms / 2;
-}
-
 template <int DT>
 cudaError_t backward(const LossGradParams &p, cudaStream_t s) {
   using gemm::Operand;
@@ -149,21 +144,18 @@ cudaError_t backward(const LossGradParams &p, cudaStream_t s) {
     // (e's rows are whole chunks: what lies past the piece's columns is written and never read)
     const typename LogitGradient<DT>::Params e{p.target, p.lse,  p.factors,
                                                tokens,   gemm::Out{p.e, p.x.padded, p.ld_e, p.ld_e, true}, v0};
-    err = gemm::launch_product<false, false, LogitGradient<DT>>(x_along, w_along, false, by_pairs(tokens, n, p.sms), DT == kBF16,
-                                                                p.status, p.sms, e, s);
+    err = gemm::launch_product<false, false, LogitGradient<DT>>(x_along, w_along, false, DT == kBF16, p.status, p.sms, e, s);
     if (err == cudaSuccess && p.dx) {
       const Operand e_along{p.e, p.x.padded, n, p.ld_e, 0, 1, false}, w_across{w, hidden, n, p.w.ld, 0, 1, true};
       const typename Summed<DT>::Params d{gemm::Out{p.dx, tokens, hidden, p.ld_dx, rows32(p.dx, p.ld_dx, 2)}, scale, p.sum_x,
                                           p.ld_sum, v0 == 0, v0 + n == vocabulary};
-      err = gemm::launch_product<false, true, Summed<DT>>(e_along, w_across, false, by_pairs(tokens, hidden, p.sms), DT == kBF16,
-                                                          p.status, p.sms, d, s);
+      err = gemm::launch_product<false, true, Summed<DT>>(e_along, w_across, false, DT == kBF16, p.status, p.sms, d, s);
     }
     if (err == cudaSuccess && p.dw) {
       const Operand e_across{p.e, n, p.x.padded, p.ld_e, 0, 1, true}, x_across{p.x.at, hidden, p.x.padded, p.x.ld, 0, 1, true};
       void *dw = static_cast<uint16_t *>(p.dw) + v0 * p.ld_dw;
       const typename Scaled<DT>::Params d{gemm::Out{dw, n, hidden, p.ld_dw, rows32(dw, p.ld_dw, 2)}, scale};
-      err = gemm::launch_product<true, true, Scaled<DT>>(e_across, x_across, false, by_pairs(n, hidden, p.sms), DT == kBF16,
-                                                         p.status, p.sms, d, s);
+      err = gemm::launch_product<true, true, Scaled<DT>>(e_across, x_across, false, DT == kBF16, p.status, p.sms, d, s);
     }
   }
   return err;

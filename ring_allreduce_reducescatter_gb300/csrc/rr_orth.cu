@@ -59,8 +59,25 @@ __device__ __forceinline__ Squares block_sum(Squares v, Squares *slots) {
   return v;
 }
 
-// blockIdx.x: one of kOrthParts parts of a matrix's rows and columns (every
-// kOrthParts-th piece of 2048 columns of a row); blockIdx.y: the matrix.
+// Eight columns of a row, zeros past the last.
+template <int DT>
+__device__ __forceinline__ void eight(const OrthParams &p, const typename Fmt<DT>::type *row, long long c, float x[8]) {
+  if (p.vec && c + 8 <= p.cols) {
+    uint4 raw[kRaw8<DT>];
+#pragma unroll
+    for (int j = 0; j < kRaw8<DT>; ++j) raw[j] = ldg_stream(reinterpret_cast<const uint4 *>(row + c) + j);
+    widen8<DT>(raw, x);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = c + j < p.cols ? to_f32<DT>(row[c + j]) : 0.f;
+  }
+}
+// Group i of `each` a row: its row.
+__device__ __forceinline__ long long row_of(long long i, long long each) {
+  return i < 0x7fffffff ? (long long)((unsigned)i / (unsigned)each) : i / each;
+}
+
+// blockIdx.x: one of p.parts parts of a matrix; blockIdx.y: the matrix.
 template <int DT>
 __global__ void __launch_bounds__(256) orth_squares_kernel(const __grid_constant__ OrthParams p) {
   using T = typename Fmt<DT>::type;
@@ -68,17 +85,13 @@ __global__ void __launch_bounds__(256) orth_squares_kernel(const __grid_constant
   grid_dependency_wait();
   grid_dependents_launch();
   const T *g = static_cast<const T *>(p.g) + blockIdx.y * p.stride_g;
-  const long long pieces = (p.cols + 2047) / 2048, all = pieces * p.rows;
+  const long long each = (p.cols + 7) / 8, all = each * p.rows, step = (long long)p.parts * 256;
   Squares v{0.f, 0.f, 0.f};
-  for (long long q = blockIdx.x; q < all; q += kOrthParts) {
-    const long long row = q / pieces, c0 = (q - row * pieces) * 2048;
-    const T *from = g + row * p.ld_g;
+#pragma unroll 4
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += step) {
+    const long long row = row_of(i, each);
     float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const long long c = c0 + threadIdx.x + 256 * j;
-      x[j] = c < p.cols ? to_f32<DT>(from[c]) : 0.f;
-    }
+    eight<DT>(p, g + row * p.ld_g, (i - row * each) * 8, x);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       v.mid = __fmaf_rn(x[j], x[j], v.mid);
@@ -90,7 +103,7 @@ __global__ void __launch_bounds__(256) orth_squares_kernel(const __grid_constant
   }
   v = block_sum(v, slots);
   if (threadIdx.x == 0) {
-    float *out = p.norms + (blockIdx.y * (long long)kOrthParts + blockIdx.x) * 3;
+    float *out = p.norms + (blockIdx.y * (long long)p.parts + blockIdx.x) * 3;
     out[0] = v.mid, out[1] = v.big, out[2] = v.small;
   }
 }
@@ -102,20 +115,30 @@ __global__ void __launch_bounds__(256) orth_start_kernel(const __grid_constant__
   __shared__ Squares slots[8];
   grid_dependency_wait();
   grid_dependents_launch();
-  static_assert(kOrthParts == 256, "one a thread");
-  const float *part = p.norms + (blockIdx.y * (long long)kOrthParts + threadIdx.x) * 3;
-  const Squares v = block_sum(Squares{part[0], part[1], part[2]}, slots);
+  Squares v{0.f, 0.f, 0.f};
+  const float *part = p.norms + blockIdx.y * (long long)p.parts * 3;
+  for (int i = threadIdx.x; i < p.parts; i += 256)
+    v.mid = __fadd_rn(v.mid, part[3 * i]), v.big = __fadd_rn(v.big, part[3 * i + 1]), v.small = __fadd_rn(v.small, part[3 * i + 2]);
+  v = block_sum(v, slots);
   const bool big = DT != kF16 && !(v.mid < 1e30f), small = DT != kF16 && v.mid < 1e-20f;
   const float before = big ? kDown : small ? kUp : 1.f;
   const float norm = __fadd_rn(__fsqrt_rn(big ? v.big : small ? v.small : v.mid), __fmul_rn(p.eps, before));
   const float scale = __fdiv_rn(kHeldX, norm);
   const T *g = static_cast<const T *>(p.g) + blockIdx.y * p.stride_g;
   __half *x = static_cast<__half *>(p.x[0]) + blockIdx.y * p.stride_x;
-  for (long long row = blockIdx.x; row < p.held_rows; row += gridDim.x) {
-    const long long cols = row < p.rows ? p.cols : 0;
-#pragma unroll 4
-    for (long long c = threadIdx.x; c < p.ld_x; c += 256)
-      x[row * p.ld_x + c] = __float2half_rn(c < cols ? __fmul_rn(__fmul_rn(to_f32<DT>(g[row * p.ld_g + c]), before), scale) : 0.f);
+  const long long each = p.ld_x / 8, all = each * p.held_rows, step = gridDim.x * 256ll;
+#pragma unroll 2
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < all; i += step) {
+    const long long row = row_of(i, each), c = (i - row * each) * 8;
+    float w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0.f;
+    if (row < p.rows && c < p.cols) eight<DT>(p, g + row * p.ld_g, c, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(__fmul_rn(w[j], before), scale);
+    uint4 raw;
+    narrow8<kF16>(w, &raw);
+    *reinterpret_cast<uint4 *>(x + row * p.ld_x + c) = raw;
   }
 }
 
@@ -185,23 +208,18 @@ cudaError_t launch(void (*k)(P...), dim3 grid, int block, cudaStream_t s, const 
 
 template <int DT>
 cudaError_t start(const OrthParams &p, cudaStream_t s) {
-  cudaError_t e = launch(orth_squares_kernel<DT>, dim3(kOrthParts, p.batch), 256, s, p);
+  cudaError_t e = launch(orth_squares_kernel<DT>, dim3((unsigned)p.parts, p.batch), 256, s, p);
   if (e != cudaSuccess) return e;
-  const long long rows = p.held_rows < 2048 ? p.held_rows : 2048;
-  return launch(orth_start_kernel<DT>, dim3((unsigned)rows, p.batch), 256, s, p);
+  const long long groups = ceil_div(p.held_rows * (p.ld_x / 8), 256ll), most = 8ll * p.sms;
+  return launch(orth_start_kernel<DT>, dim3((unsigned)(groups < most ? groups : most), p.batch), 256, s, p);
 }
-
-// The larger tiles once every pair of SMs has one.
-bool by_pairs(long long tiles, int sms) { return tiles >= sms / 2; }
-long long tiles_of(long long m, long long n, long long side) { return ceil_div(m, side) * ceil_div(n, side); }
 
 template <bool kMnA, bool kMnB, int DT>
 cudaError_t product(const OrthParams &p, const gemm::Operand &a, const gemm::Operand &b, bool upper,
                     typename Combined<DT>::Params e, cudaStream_t s) {
-  const long long t = ceil_div(a.rows, 256ll), tiles = (upper ? t * (t + 1) / 2 : tiles_of(a.rows, b.rows, 256)) * p.batch;
-  const bool pair = by_pairs(tiles, p.sms);
-  if (upper) e.tile = pair ? 256 : 128;
-  return gemm::launch_product<kMnA, kMnB, Combined<DT>>(a, b, upper, pair, 0, p.status, p.sms, e, s);
+  int split;
+  if (upper) e.tile = gemm::kind_of(a.rows, b.rows, a.k, b.batch, true, p.sms, &split) == gemm::kPair ? 256 : 128;
+  return gemm::launch_product<kMnA, kMnB, Combined<DT>>(a, b, upper, 0, p.status, p.sms, e, s);
 }
 
 // X <- a X + (b S + c S^2) X, or the same from the right, to `out`.

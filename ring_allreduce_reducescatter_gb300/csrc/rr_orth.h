@@ -13,16 +13,21 @@ struct OrthParams {
   const void *g;
   void *out;
   long long rows, cols, ld_g, ld_out, stride_g, stride_out;  // strides: from matrix to matrix
-  int batch, steps, dtype, out_dtype;
+  int batch, steps, dtype, out_dtype, parts;
+  bool vec;  // 16-byte groups of the rows of g are aligned
   float eps;
-  float *norms;       // [batch][kOrthParts][3]
+  float *norms;       // [batch][parts][3]
   void *x[2], *s, *b; // binary16: two iterates, the Gram matrix and its polynomial
   long long held_rows, held_cols, ld_x, ld_s, stride_x, stride_s;
   unsigned int *status;
   int sms;
 };
 
-constexpr int kOrthParts = 256;  // partial sums of a matrix's squares
+// Partial sums of a matrix's squares: 2048 elements each at least.
+inline int orth_parts(long long rows, long long cols) {
+  const long long n = ceil_div(rows * cols, 2048ll);
+  return (int)(n < 1024 ? n : 1024);
+}
 
 // The sizes that the iterates are held in: small ones in whole boxes of zeros and
 // elements (rr_gemm.cuh says why).

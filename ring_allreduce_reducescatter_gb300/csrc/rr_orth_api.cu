@@ -31,7 +31,7 @@ struct Layout {
     const size_t m = held_rows < held_cols ? held_rows : held_cols;
     ld_x = round_up(held_cols, 32), ld_s = round_up(m, 32);
     stride_x = held_rows * ld_x, stride_s = m * ld_s;
-    norms = take(batch * rr::kOrthParts * 12);
+    norms = take(batch * (size_t)rr::orth_parts((long long)rows, (long long)cols) * 12);
     for (size_t &at : x) at = take(batch * stride_x * 2);
     s = take(batch * stride_s * 2);
     b = take(batch * stride_s * 2);
@@ -85,6 +85,8 @@ rr_status ring_orthogonalize(const void *g, size_t ld_g, size_t stride_g, rr_dty
   p.stride_g = batch > 1 ? (long long)stride_g : 0, p.stride_out = batch > 1 ? (long long)stride_out : 0;
   p.batch = (int)batch, p.steps = steps, p.dtype = dtype, p.out_dtype = out_dtype;
   p.eps = (float)eps;
+  p.parts = rr::orth_parts(p.rows, p.cols);
+  p.vec = rr::aligned16(g, rows, ld_g, elem_bytes(dtype)) && (batch == 1 || stride_g * elem_bytes(dtype) % 16 == 0);
   p.norms = reinterpret_cast<float *>(ws + l.norms);
   p.x[0] = ws + l.x[0], p.x[1] = ws + l.x[1], p.s = ws + l.s, p.b = ws + l.b;
   p.held_rows = (long long)l.held_rows, p.held_cols = (long long)l.held_cols;

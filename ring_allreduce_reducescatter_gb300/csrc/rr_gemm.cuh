@@ -45,23 +45,30 @@ using Single = Shape<1, 128>;
 
 struct Product {
   CUtensorMap a, b;  // (inner axis, outer axis, batch)
+  CUtensorMap b_half;  // b in half the rows a box (halved tiles of pairs)
   long long m, n;
   int steps;  // of K
   int tiles_m, tiles_n;
-  long long per_batch, items;  // tiles of one product, and of all
+  long long per_batch;         // tiles of one product
+  long long items, whole;      // pieces of work, of which the first are whole tiles, the rest halves
   uint32_t format;             // of the operands: 0 binary16, 1 bfloat16
+  uint32_t bytes_a;            // of A's box of one step (single tiles of few rows: the rows there are)
   int upper;                   // D is symmetric: only tiles on and above the diagonal
   unsigned int *status;
 };
 
 struct Place {
   int batch, tm, tn;
+  bool whole;
+  int side;  // of the columns of a halved tile
 };
-// Tile t.  Eight rows of tiles go together, column after column, so that the
+// Piece t of the work: a tile, or half of one.  Eight rows of tiles go together, column after column, so that the
 // tiles in flight share their operands in L2; of a symmetric product, the
 // columns of the upper triangle.
 __device__ __forceinline__ Place place_of(const Product &p, long long t) {
   Place w;
+  w.whole = t < p.whole, w.side = w.whole ? 0 : (int)((t - p.whole) & 1);
+  if (!w.whole) t = p.whole + (t - p.whole) / 2;
   w.batch = (int)(t / p.per_batch);
   const int u = (int)(t - w.batch * p.per_batch);
   if (p.upper) {
@@ -129,6 +136,11 @@ __device__ __forceinline__ void load_box(void *dst, const CUtensorMap *map, int 
   }
 }
 
+// Brings a tensor map to where the copies read it, ahead of the first (one thread).
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // Waits for this warp's tensor-memory loads; the values, named here, cannot be
 // used before.
 __device__ __forceinline__ void tmem_loaded32(uint32_t r[32]) {
@@ -172,6 +184,7 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
     for (int s = 0; s < 2; ++s) mbar_init(&acc_full[s], 1), mbar_init(&acc_empty[s], 8 * G);
     fence_mbar_init();
   }
+  if (threadIdx.x == 256) prefetch_map(&p.a), prefetch_map(&p.b);
   if (warp == 9) tmem_alloc<G>(&tmem_slot, S::kColumns);
   tcgen05_fence_before();
   __syncthreads();
@@ -191,8 +204,9 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
     for (long long t = worker; t < p.items; t += workers, ++i) {
       const Place w = place_of(p, t);
       const unsigned buf = i & 1;
-      Epi epi(e, (long long)w.tm * S::kBM + rank * 128 + quarter * 32 + lane, (long long)w.tn * S::kBN + half * S::kHalf,
-              w.batch, stage);
+      const bool mine = G == 1 || w.whole || half == 0;  // a half tile is one half's warps' work
+      Epi epi(e, (long long)w.tm * S::kBM + rank * 128 + quarter * 32 + lane,
+              (long long)w.tn * S::kBN + (G == 1 || w.whole ? half : w.side) * S::kHalf, w.batch, stage);
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1, kWaitLimitNs))) {
         if (lane == 0) atomicOr(p.status, kStatusWaitTimeout);
         break;
@@ -200,21 +214,25 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
       tcgen05_fence_after();
       const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * S::kBN + half * S::kHalf;
       constexpr int kChunks = S::kHalf / kChunk;
+      const auto release = [&] {
+        tcgen05_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (G == 2) cluster_arrive_remote(cluster_addr(&acc_empty[buf], 0));
+          else asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&acc_empty[buf])) : "memory");
+        }
+      };
+      if (!mine) {
+        release();
+        continue;
+      }
       uint32_t acc[2][kChunk];  // a chunk is on its way while the one before is worked on
       tmem_load32(at, acc[0]);
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         tmem_loaded32(acc[c & 1]);
-        if (c + 1 < kChunks) {
-          tmem_load32(at + (c + 1) * kChunk, acc[(c + 1) & 1]);
-        } else {
-          tcgen05_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (G == 2) cluster_arrive_remote(cluster_addr(&acc_empty[buf], 0));
-            else asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&acc_empty[buf])) : "memory");
-          }
-        }
+        if (c + 1 < kChunks) tmem_load32(at + (c + 1) * kChunk, acc[(c + 1) & 1]);
+        else release();
         float v[kChunk];
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) v[j] = __uint_as_float(acc[c & 1][j]);
@@ -234,7 +252,9 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
       bool ok = true;
       for (long long t = worker; t < p.items && ok; t += workers) {
         const Place w = place_of(p, t);
-        const int row_a = w.tm * S::kBM + (int)rank * 128, row_b = w.tn * S::kBN + (int)rank * S::kRowsB;
+        const int row_a = w.tm * S::kBM + (int)rank * 128, row_b = w.tn * S::kBN + (G == 1 || w.whole ? (int)rank * S::kRowsB : w.side * S::kHalf + (int)rank * S::kRowsB / 2);
+        const bool whole = G == 1 || w.whole;
+        const uint32_t bytes = G * (p.bytes_a + (whole ? S::kBytesB : S::kBytesB / 2));
         for (int k = 0; k < p.steps; ++k, ++g) {
           const unsigned s = g % S::kStages;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((g / S::kStages) & 1) ^ 1, kWaitLimitNs)))) break;
@@ -242,7 +262,7 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
           const uint32_t bar = G == 2 ? cluster_addr(&full[s], 0) : 0;
           if (one) {
             // (what lies past the operands' ends reads as zeros and counts)
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], G * S::kStageBytes);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
             if constexpr (kMnA) {
 #pragma unroll
               for (int j = 0; j < 2; ++j) load_box<G>(a + 8192 * j, &p.a, row_a + 64 * j, k * kStep, w.batch, &full[s], bar, pol);
@@ -252,9 +272,9 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
             if constexpr (kMnB) {
 #pragma unroll
               for (int j = 0; j < S::kRowsB / 64; ++j)
-                load_box<G>(b + 8192 * j, &p.b, row_b + 64 * j, k * kStep, w.batch, &full[s], bar, pol);
+                if (j == 0 || whole) load_box<G>(b + 8192 * j, &p.b, row_b + 64 * j, k * kStep, w.batch, &full[s], bar, pol);
             } else {
-              load_box<G>(b, &p.b, k * kStep, row_b, w.batch, &full[s], bar, pol);
+              load_box<G>(b, whole ? &p.b : &p.b_half, k * kStep, row_b, w.batch, &full[s], bar, pol);
             }
           }
           __syncwarp();
@@ -266,7 +286,6 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
       if (rank == 0) wait_turns<S::kStages>(full, g, kWaitLimitNs);
     } else if (warp == 9 && rank == 0) {
       const bool one = elect_one();
-      const uint32_t idesc = instr_desc(p.format, kMnA, kMnB, S::kBM, S::kBN);
       unsigned g = 0, i = 0;
       bool ok = true;
       for (long long t = worker; t < p.items && ok; t += workers, ++i) {
@@ -274,6 +293,8 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
         if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty[buf], ((i >> 1) & 1) ^ 1, kWaitLimitNs)))) break;
         tcgen05_fence_after();
         const uint32_t d = tmem + buf * S::kBN;
+        const uint32_t idesc = G == 1 || t < p.whole ? instr_desc(p.format, kMnA, kMnB, S::kBM, S::kBN)
+                                                     : instr_desc(p.format, kMnA, kMnB, S::kBM, S::kBN / 2);
         for (int k = 0; k < p.steps; ++k, ++g) {
           const unsigned s = g % S::kStages;
           if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (g / S::kStages) & 1, kWaitLimitNs)))) break;
@@ -342,6 +363,7 @@ __global__ void __launch_bounds__(Split::kThreads, 1)
     fence_mbar_init();
   }
   cluster_arrive();  // waited for before the first remote store: by then every CTA runs
+  if (threadIdx.x == 256) prefetch_map(&p.a), prefetch_map(&p.b);
   if (warp == 9) tmem_alloc<1>(&tmem_slot, Split::kColumns);
   tcgen05_fence_before();
   __syncthreads();
@@ -362,7 +384,7 @@ __global__ void __launch_bounds__(Split::kThreads, 1)
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(&empty[s], ((k / Split::kStages) & 1) ^ 1, kWaitLimitNs))) break;
       unsigned char *a = smem + s * Split::kStageBytes, *b = a + 128 * 128;
       if (one) {
-        mbar_arrive_expect_tx(&full[s], Split::kStageBytes);
+        mbar_arrive_expect_tx(&full[s], p.bytes_a + 128 * 128);
         if constexpr (kMnA) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) load_box<1>(a + 8192 * j, &p.a, w.tm * 128 + 64 * j, (k0 + k) * kStep, w.batch, &full[s], 0, pol);
@@ -542,7 +564,8 @@ struct Operand {
 // Boxes that lie partly past the end of a small operand are slow to read when all
 // SMs read it: 16 rows by 1024 (32 KB) in boxes of 128 rows took a product with
 // 131072 rows 252 us, in an array of 256 KB 77 us, 128 whole rows 66 us.  Small
-// operands therefore lie in whole boxes, of rows and of zeros.
+// operands therefore lie in whole boxes, of rows and of zeros, or the box is as high
+// as the operand.
 constexpr long long kSmallOperand = 1 << 20;  // bytes
 
 // Defined in rr_gemm.cu: the map of an operand's boxes; `box` rows a box along K.
@@ -551,11 +574,15 @@ bool make_operand_map(CUtensorMap *map, const Operand &o, int box);
 template <class S>
 bool fill_product(Product *q, const Operand &a, const Operand &b, bool upper, uint32_t format, unsigned int *status) {
   q->m = a.rows, q->n = b.rows;
-  if (!make_operand_map(&q->a, a, 128) || !make_operand_map(&q->b, b, S::kRowsB)) return false;
+  // (rows of A that are not there leave what shared memory held in rows of D that
+  // no epilogue stores)
+  const int box = !a.mn && S::kBM == 128 && a.rows < 128 ? (int)a.rows : 128;
+  if (!make_operand_map(&q->a, a, box) || !make_operand_map(&q->b, b, S::kRowsB)) return false;
+  q->bytes_a = (uint32_t)box * 128;
   q->steps = (int)ceil_div(a.k, (long long)kStep);
   q->tiles_m = (int)ceil_div(q->m, (long long)S::kBM), q->tiles_n = (int)ceil_div(q->n, (long long)S::kBN);
   q->per_batch = upper ? (long long)q->tiles_n * (q->tiles_n + 1) / 2 : (long long)q->tiles_m * q->tiles_n;
-  q->items = q->per_batch * b.batch;
+  q->items = q->whole = q->per_batch * b.batch;
   q->format = format, q->upper = upper, q->status = status;
   return true;
 }
@@ -565,6 +592,14 @@ cudaError_t launch_shape(const Operand &a, const Operand &b, bool upper, uint32_
                          const Params &e, cudaStream_t s) {
   Product q;
   if (!fill_product<S>(&q, a, b, upper, format, status)) return cudaErrorInvalidValue;
+  if constexpr (G == 2) {
+    // the last turn's tiles are halved where they are no more than half the pairs
+    const long long last = q.items % (sms / 2);
+    if (last > 0 && 2 * last <= sms / 2) {
+      if (!make_operand_map(&q.b_half, b, S::kRowsB / 2)) return cudaErrorInvalidValue;
+      q.whole = q.items - last, q.items += last;
+    }
+  }
   const long long most = sms / G, workers = q.items < most ? q.items : most;
   const cudaError_t err = allow_smem<kKernel>(S::kSmem);
   if (err != cudaSuccess) return err;
@@ -613,9 +648,9 @@ cudaError_t launch_split(const Operand &a, const Operand &b, bool upper, int spl
   return cudaLaunchKernelEx(&c, product_split_kernel<kMnA, kMnB, Epi>, q, e, split);
 }
 
-// Which of the three a product takes.  The larger tiles once every pair of SMs has
-// one, or where the last turn of the smaller ones would cost more: a pair's turn
-// takes 1.5 times a single's.
+// Which of the three a product takes: beyond one turn of the smaller tiles, the
+// larger ones unless their turns cost more (half a turn of a pair takes 1.33 of a
+// single's: 32 KB a step for 128 x 128 come at 64 bytes a cycle, and 24 for twice that).
 enum Kind { kSingle, kPair, kSplit };
 inline Kind kind_of(long long m, long long n, long long k, int batch, bool upper, int sms, int *split) {
   const auto tiles = [&](long long side) {
@@ -625,7 +660,9 @@ inline Kind kind_of(long long m, long long n, long long k, int batch, bool upper
   const long long pairs = tiles(256), singles = tiles(128);
   *split = split_of(singles, ceil_div(k, (long long)kStep), sms);
   if (*split > 1) return kSplit;
-  return 3 * ceil_div(pairs, (long long)sms / 2) <= 2 * ceil_div(singles, (long long)sms) ? kPair : kSingle;
+  if (singles <= sms) return kSingle;
+  const long long last = pairs % (sms / 2), turns = 2 * (pairs / (sms / 2)) + (last == 0 ? 0 : 2 * last <= sms / 2 ? 1 : 2);  // halves
+  return 3 * turns <= 4 * ceil_div(singles, (long long)sms) ? kPair : kSingle;
 }
 
 // A product of a (its rows are D's rows) and b (D's columns).  upper: D is

@@ -140,44 +140,34 @@ __global__ void __launch_bounds__(1024) loss_sums_kernel(const __grid_constant__
   p.sums[2] = count ? __fdiv_rn(total, (float)count) : 0.f;
 }
 
-// What each token's loss passes on, as the factor of its row of the logits'
-// gradient, 0 for a token that does not count and NaN for a target outside the
-// vocabulary; and the factor of the outputs.  One gradient for all tokens goes to
-// the outputs whole, so that e is p - 1 and p themselves (their common factor
-// rounded into every e put the same error, up to half a step, on all of them: twice
-// the error of dx).  Gradients of their own go over a common power of two, that of
-// the largest.  In binary16 e is 2^14 times as large: it neither overflows nor
-// falls among the subnormals, down to probabilities of 2^-28.
+// The factors of the rows of the logits' gradient for tokens that have gradients of
+// their own: over a common power of two, that of the largest, 0 for a token that
+// does not count and NaN for a target outside the vocabulary.  The outputs get the
+// power of two back.
 __global__ void __launch_bounds__(1024) loss_factors_kernel(const __grid_constant__ LossGradParams p) {
   __shared__ float tops[32];
   grid_dependency_wait();
   grid_dependents_launch();
   const long long tokens = p.x.rows;
-  const float widen = p.dtype == kF16 ? 16384.f : 1.f;
-  float down = widen, up = 1.f;
-  if (p.grad_step == 0) {
-    up = __fdiv_rn(p.grad[0], widen);
-  } else {
-    float top = 0.f;
+  const float widen = p.dtype == kF16 ? kLossWiden : 1.f;
+  float top = 0.f;
 #pragma unroll 4
-    for (long long t = threadIdx.x; t < tokens; t += 1024)
-      if (p.target[t] != p.ignore) top = fmaxf(top, fabsf(p.grad[t]));
+  for (long long t = threadIdx.x; t < tokens; t += 1024)
+    if (p.target[t] != p.ignore) top = fmaxf(top, fabsf(p.grad[t]));
 #pragma unroll
-    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
-    __syncthreads();
-    for (int w = 0; w < 32; ++w) top = fmaxf(top, tops[w]);
-    // 2^k with top <= 2^k, k in -100 .. 100; 1 where there is nothing to scale
-    int k = 0;
-    if (top > 0.f && top < INFINITY) frexpf(top, &k);
-    k = k < -100 ? -100 : k > 100 ? 100 : k;
-    down = __fmul_rn(__int_as_float((127 - k) << 23), widen), up = __fdiv_rn(__int_as_float((127 + k) << 23), widen);
-  }
+  for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = top;
+  __syncthreads();
+  for (int w = 0; w < 32; ++w) top = fmaxf(top, tops[w]);
+  // 2^k with top <= 2^k, k in -100 .. 100; 1 where there is nothing to scale
+  int k = 0;
+  if (top > 0.f && top < INFINITY) frexpf(top, &k);
+  k = k < -100 ? -100 : k > 100 ? 100 : k;
+  const float down = __fmul_rn(__int_as_float((127 - k) << 23), widen), up = __fdiv_rn(__int_as_float((127 + k) << 23), widen);
 #pragma unroll 4
   for (long long t = threadIdx.x; t < tokens; t += 1024) {
     const long long at = p.target[t];
-    const float g = p.grad_step == 0 ? widen : __fmul_rn(p.grad[t], down);
-    p.factors[t] = at == p.ignore ? 0.f : at >= 0 && at < p.w.rows ? g : NAN;
+    p.factors[t] = at == p.ignore ? 0.f : at >= 0 && at < p.w.rows ? __fmul_rn(p.grad[t], down) : NAN;
   }
   if (threadIdx.x == 0) p.factors[tokens] = up;
 }

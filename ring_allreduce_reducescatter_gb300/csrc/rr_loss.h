@@ -53,10 +53,13 @@ struct PadParams {
   long long rows_to;  // zeros behind the rows, and behind the columns up to ld_to
 };
 
+constexpr float kLossWiden = 16384.f;  // what the logits' gradient is held times in binary16
+
 // The rows that x is held in: few and short ones in whole boxes (rr_gemm.cuh says
 // why), with zeros behind them.
-inline long long loss_rows(long long tokens, long long hidden) {
-  return tokens % 128 && tokens * hidden * 2 < (1 << 20) ? ceil_div(tokens, 128ll) * 128 : tokens;
+// Where x is read along K alone, a box takes as many rows as there are up to 128.
+inline long long loss_rows(long long tokens, long long hidden, bool along) {
+  return !(along && tokens < 128) && tokens % 128 && tokens * hidden * 2 < (1 << 20) ? ceil_div(tokens, 128ll) * 128 : tokens;
 }
 
 // Whether the logits of so many tokens are made in the larger tiles, whose

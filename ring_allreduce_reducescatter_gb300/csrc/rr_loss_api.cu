@@ -34,10 +34,10 @@ struct Operands {
 };
 bool readable(const void *p, size_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
 Operands operands(Layout *l, const void *x, size_t ld_x, const void *w, size_t ld_w, size_t tokens, size_t hidden,
-                  size_t vocabulary) {
+                  size_t vocabulary, bool along) {
   Operands o{};
   o.ld = round_up(hidden, 8);
-  o.rows = (size_t)rr::loss_rows((long long)tokens, (long long)hidden);
+  o.rows = (size_t)rr::loss_rows((long long)tokens, (long long)hidden, along);
   o.copy_x = o.rows != tokens || !readable(x, ld_x), o.copy_w = !readable(w, ld_w);
   if (o.copy_x) o.x_at = l->take(o.rows * o.ld * 2);
   if (o.copy_w) o.w_at = l->take(vocabulary * o.ld * 2);
@@ -51,7 +51,7 @@ struct ForwardLayout : Layout {
     const size_t group = (size_t)rr::loss_group((long long)tokens);
     parts = take((vocabulary + group - 1) / group * tokens * 8);
     chosen = take(tokens * 4);
-    o = operands(this, x, ld_x, w, ld_w, tokens, hidden, vocabulary);
+    o = operands(this, x, ld_x, w, ld_w, tokens, hidden, vocabulary, true);
   }
 };
 struct BackwardLayout : Layout {
@@ -61,9 +61,9 @@ struct BackwardLayout : Layout {
     piece = (size_t)rr::loss_piece((long long)tokens, (long long)vocabulary);
     ld_sum = round_up(hidden, 32);
     factors = take((tokens + 1) * 4);
-    e = take((size_t)rr::loss_rows((long long)tokens, (long long)hidden) * piece * 2);
+    e = take((size_t)rr::loss_rows((long long)tokens, (long long)hidden, false) * piece * 2);
     sum = piece < vocabulary ? take(tokens * ld_sum * 4) : 0;
-    o = operands(this, x, ld_x, w, ld_w, tokens, hidden, vocabulary);
+    o = operands(this, x, ld_x, w, ld_w, tokens, hidden, vocabulary, false);
   }
 };
 

@@ -30,7 +30,10 @@ template <int DT>
 struct LogitGradient {
   struct Params {
     const long long *target;
-    const float *lse, *factors;
+    const float *lse;
+    const float *factors;  // null: `widen` for a token that counts
+    long long ignore, vocabulary;
+    float widen;
     long long tokens;
     gemm::Out e;      // (rows past the tokens: zeros)
     long long first;  // the piece's first column of the vocabulary
@@ -40,7 +43,11 @@ struct LogitGradient {
   float lse, factor, *stage;
   __device__ __forceinline__ LogitGradient(const Params &p, long long row, long long col, int, float *stage)
       : p(p), row(row), col(col), at(-1), lse(0.f), factor(0.f), stage(stage) {
-    if (row < p.tokens) at = p.target[row] - p.first, lse = p.lse[row], factor = p.factors[row];
+    if (row < p.tokens) {
+      at = p.target[row], lse = p.lse[row];
+      factor = p.factors ? p.factors[row] : at == p.ignore ? 0.f : at >= 0 && at < p.vocabulary ? p.widen : NAN;
+      at -= p.first;
+    }
   }
   __device__ __forceinline__ void chunk(int c, float v[gemm::kChunk]) {
     const long long first = col + c * gemm::kChunk;
@@ -68,12 +75,13 @@ struct Scaled {
   struct Params {
     gemm::Out out;
     const float *scale;
+    float narrow;  // scale times this
   };
   const Params &p;
   long long row, col;
   float scale, *stage;
   __device__ __forceinline__ Scaled(const Params &p, long long row, long long col, int, float *stage)
-      : p(p), row(row), col(col), scale(*p.scale), stage(stage) {}
+      : p(p), row(row), col(col), scale(__fmul_rn(*p.scale, p.narrow)), stage(stage) {}
   __device__ __forceinline__ void chunk(int c, float v[gemm::kChunk]) {
 #pragma unroll
     for (int j = 0; j < gemm::kChunk; ++j) v[j] = __fmul_rn(v[j], scale);
@@ -88,6 +96,7 @@ struct Summed {
   struct Params {
     gemm::Out out;
     const float *scale;
+    float narrow;
     float *sum;  // rows of ld_sum, a multiple of 32
     long long ld_sum;
     bool first, last;
@@ -96,7 +105,7 @@ struct Summed {
   long long row, col;
   float scale, *stage;
   __device__ __forceinline__ Summed(const Params &p, long long row, long long col, int, float *stage)
-      : p(p), row(row), col(col), scale(*p.scale), stage(stage) {}
+      : p(p), row(row), col(col), scale(__fmul_rn(*p.scale, p.narrow)), stage(stage) {}
   __device__ __forceinline__ void chunk(int c, float v[gemm::kChunk]) {
     const long long at = col + c * gemm::kChunk;
     if (at >= p.out.cols) return;
@@ -135,26 +144,34 @@ template <int DT>
 cudaError_t backward(const LossGradParams &p, cudaStream_t s) {
   using gemm::Operand;
   const long long tokens = p.x.rows, vocabulary = p.w.rows, hidden = p.hidden;
-  cudaError_t err = launch_loss_factors(p, s);
-  const float *scale = p.factors + tokens;
+  // One gradient for all tokens goes to the outputs whole, so that e is p - 1 and p
+  // themselves (their common factor rounded into every e put the same error, up to
+  // half a step, on all of them: twice the error of dx).  Gradients of their own make
+  // factors.  In binary16 e is 2^14 times as large: it neither overflows nor falls
+  // among the subnormals, down to probabilities of 2^-28.
+  const bool one = p.grad_step == 0;
+  const float widen = DT == kF16 ? kLossWiden : 1.f, narrow = one ? 1.f / widen : 1.f;
+  cudaError_t err = one ? cudaSuccess : launch_loss_factors(p, s);
+  const float *scale = one ? p.grad : p.factors + tokens;
   for (long long v0 = 0; v0 < vocabulary && err == cudaSuccess; v0 += p.piece) {
     const long long n = vocabulary - v0 < p.piece ? vocabulary - v0 : p.piece;
     const void *w = static_cast<const uint16_t *>(p.w.at) + v0 * p.w.ld;
     const Operand x_along{p.x.at, p.x.padded, hidden, p.x.ld, 0, 1, false}, w_along{w, n, hidden, p.w.ld, 0, 1, false};
     // (e's rows are whole chunks: what lies past the piece's columns is written and never read)
-    const typename LogitGradient<DT>::Params e{p.target, p.lse,  p.factors,
-                                               tokens,   gemm::Out{p.e, p.x.padded, p.ld_e, p.ld_e, true}, v0};
+    const typename LogitGradient<DT>::Params e{p.target,   p.lse,      one ? nullptr : p.factors,
+                                               p.ignore,   vocabulary, widen,
+                                               tokens,     gemm::Out{p.e, p.x.padded, p.ld_e, p.ld_e, true}, v0};
     err = gemm::launch_product<false, false, LogitGradient<DT>>(x_along, w_along, false, DT == kBF16, p.status, p.sms, e, s);
     if (err == cudaSuccess && p.dx) {
       const Operand e_along{p.e, p.x.padded, n, p.ld_e, 0, 1, false}, w_across{w, hidden, n, p.w.ld, 0, 1, true};
-      const typename Summed<DT>::Params d{gemm::Out{p.dx, tokens, hidden, p.ld_dx, rows32(p.dx, p.ld_dx, 2)}, scale, p.sum_x,
+      const typename Summed<DT>::Params d{gemm::Out{p.dx, tokens, hidden, p.ld_dx, rows32(p.dx, p.ld_dx, 2)}, scale, narrow, p.sum_x,
                                           p.ld_sum, v0 == 0, v0 + n == vocabulary};
       err = gemm::launch_product<false, true, Summed<DT>>(e_along, w_across, false, DT == kBF16, p.status, p.sms, d, s);
     }
     if (err == cudaSuccess && p.dw) {
       const Operand e_across{p.e, n, p.x.padded, p.ld_e, 0, 1, true}, x_across{p.x.at, hidden, p.x.padded, p.x.ld, 0, 1, true};
       void *dw = static_cast<uint16_t *>(p.dw) + v0 * p.ld_dw;
-      const typename Scaled<DT>::Params d{gemm::Out{dw, n, hidden, p.ld_dw, rows32(dw, p.ld_dw, 2)}, scale};
+      const typename Scaled<DT>::Params d{gemm::Out{dw, n, hidden, p.ld_dw, rows32(dw, p.ld_dw, 2)}, scale, narrow};
       err = gemm::launch_product<true, true, Scaled<DT>>(e_across, x_across, false, DT == kBF16, p.status, p.sms, d, s);
     }
   }

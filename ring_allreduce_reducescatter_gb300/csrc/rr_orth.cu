@@ -152,6 +152,7 @@ struct Combined {
     long long ld_c, c_stride;
     float alpha, beta;
     int tile;  // rows of a tile of a symmetric D (else 0)
+    int half;  // columns of an epilogue
   };
   const Params &p;
   gemm::Out out;
@@ -159,27 +160,33 @@ struct Combined {
   long long row, col;
   float *stage;
   bool mirror;
+  uint4 next[4];  // C's chunk that comes next, on its way since the one before
   __device__ __forceinline__ Combined(const Params &p, long long row, long long col, int batch, float *stage)
       : p(p), out(p.out), c0(p.c ? p.c + batch * p.c_stride + row * p.ld_c + col : nullptr), row(row), col(col), stage(stage),
         mirror(p.tile && row / p.tile != col / p.tile) {
     out.at = static_cast<typename Fmt<DT>::type *>(p.out.at) + batch * p.out_stride;
+    fetch(0);
+  }
+  // (C's rows are whole chunks)
+  __device__ __forceinline__ void fetch(int c) {
+    if (!c0 || row >= out.rows || col + c * gemm::kChunk >= out.cols) return;
+    ldg32(c0 + c * gemm::kChunk, next[0], next[1]);
+    ldg32(c0 + c * gemm::kChunk + 16, next[2], next[3]);
   }
   __device__ __forceinline__ void chunk(int c, float v[gemm::kChunk]) {
     const long long at = col + c * gemm::kChunk;
     if (at >= out.cols) return;
 #pragma unroll
     for (int j = 0; j < gemm::kChunk; ++j) v[j] = __fmul_rn(v[j], p.alpha);
-    if (c0 && row < out.rows) {  // (C's rows are whole chunks)
-      uint4 raw[4];
-      ldg32(c0 + c * gemm::kChunk, raw[0], raw[1]);
-      ldg32(c0 + c * gemm::kChunk + 16, raw[2], raw[3]);
+    if (c0 && row < out.rows) {
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         float w[8];
-        widen8<kF16>(raw + h, w);
+        widen8<kF16>(next + h, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[8 * h + j] = __fmaf_rn(w[j], p.beta, v[8 * h + j]);
       }
+      if ((c + 1) * gemm::kChunk < p.half) fetch(c + 1);
     }
     gemm::store_row<DT>(out, row, at, v, stage);
     if (mirror && row < out.rows) {
@@ -218,7 +225,9 @@ template <bool kMnA, bool kMnB, int DT>
 cudaError_t product(const OrthParams &p, const gemm::Operand &a, const gemm::Operand &b, bool upper,
                     typename Combined<DT>::Params e, cudaStream_t s) {
   int split;
-  if (upper) e.tile = gemm::kind_of(a.rows, b.rows, a.k, b.batch, true, p.sms, &split) == gemm::kPair ? 256 : 128;
+  const gemm::Kind kind = gemm::kind_of(a.rows, b.rows, a.k, b.batch, upper, p.sms, &split);
+  if (upper) e.tile = kind == gemm::kPair ? 256 : 128;
+  e.half = kind == gemm::kPair ? gemm::Pair::kHalf : kind == gemm::kSingle ? gemm::Single::kHalf : gemm::kChunk;
   return gemm::launch_product<kMnA, kMnB, Combined<DT>>(a, b, upper, 0, p.status, p.sms, e, s);
 }
 
@@ -228,7 +237,7 @@ cudaError_t update(const OrthParams &p, const void *x, const gemm::Out &out, lon
                    cudaStream_t s) {
   using gemm::Operand;
   const long long m = p.held_rows < p.held_cols ? p.held_rows : p.held_cols;
-  const typename Combined<DT>::Params e{out, out_stride, static_cast<const __half *>(x), p.ld_x, p.stride_x, alpha, beta, 0};
+  const typename Combined<DT>::Params e{out, out_stride, static_cast<const __half *>(x), p.ld_x, p.stride_x, alpha, beta, 0, 0};
   const Operand poly{p.b, m, m, p.ld_s, p.stride_s, p.batch, false};
   if (p.rows > p.cols) {
     const Operand along{x, p.held_rows, p.held_cols, p.ld_x, p.stride_x, p.batch, false};
@@ -250,7 +259,7 @@ cudaError_t launch_orth(const OrthParams &p, cudaStream_t s) {
   const float into_s = kHeldS / (kHeldX * kHeldX);
   for (int k = 0; k < p.steps && err == cudaSuccess; ++k) {
     const void *x = p.x[k & 1];
-    const Combined<kF16>::Params es{held_s, p.stride_s, nullptr, 0, 0, into_s, 0.f, 0};
+    const Combined<kF16>::Params es{held_s, p.stride_s, nullptr, 0, 0, into_s, 0.f, 0, 0};
     if (tall) {
       const Operand across{x, p.held_cols, p.held_rows, p.ld_x, p.stride_x, p.batch, true};
       err = product<true, true, kF16>(p, across, across, true, es, s);
@@ -261,7 +270,7 @@ cudaError_t launch_orth(const OrthParams &p, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     const Operand gram{p.s, m, m, p.ld_s, p.stride_s, p.batch, false};
     const Combined<kF16>::Params eb{held_b, p.stride_s, static_cast<const __half *>(p.s), p.ld_s, p.stride_s,
-                                    kC * kHeldB / (kHeldS * kHeldS), kB * kHeldB / kHeldS, 0};
+                                    kC * kHeldB / (kHeldS * kHeldS), kB * kHeldB / kHeldS, 0, 0};
     if ((err = product<false, false, kF16>(p, gram, gram, true, eb, s)) != cudaSuccess) return err;
     if (k + 1 < p.steps) {
       err = update<kF16>(p, x, Out{p.x[(k + 1) & 1], p.held_rows, p.ld_x, p.ld_x, true}, p.stride_x, 1.f / kHeldB, kA, s);

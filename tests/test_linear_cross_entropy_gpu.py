@@ -92,7 +92,7 @@ def check_gradients(dx, dw, grad, x, w, target, l, ignore=-100):
 
 
 SHAPES = [(1, 64, 500), (1, 1, 1), (3, 8, 2), (5, 16, 64), (33, 129, 1000), (128, 64, 130), (129, 64, 257), (130, 777, 523),
-          (300, 96, 5003), (1000, 200, 129), (257, 72, 20000), (64, 1024, 8000), (2500, 320, 2500)]
+          (300, 96, 5003), (1000, 200, 129), (257, 72, 20000), (64, 1024, 8000), (2500, 320, 2500), (2300, 2320, 2330)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])

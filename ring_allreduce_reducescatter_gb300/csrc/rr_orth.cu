@@ -24,40 +24,13 @@
 #include <math.h>
 
 #include "rr_gemm.cuh"
-#include "rr_orth.h"
+#include "rr_orth.cuh"
 
 namespace rr {
 
 namespace {
 
-constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-constexpr float kHeldX = 64.f, kHeldS = 16384.f, kHeldB = 8192.f;  // what each is held times
-
-// Sums of squares of x, x 2^-60 and x 2^60: one of them neither overflows nor
-// loses its terms, whatever the matrix's scale.
-constexpr float kDown = 0x1p-60f, kUp = 0x1p60f;
-
-struct Squares {
-  float mid, big, small;
-};
-__device__ __forceinline__ Squares block_sum(Squares v, Squares *slots) {
-#pragma unroll
-  for (int d = 16; d > 0; d /= 2) {
-    v.mid = __fadd_rn(v.mid, __shfl_xor_sync(0xffffffffu, v.mid, d));
-    v.big = __fadd_rn(v.big, __shfl_xor_sync(0xffffffffu, v.big, d));
-    v.small = __fadd_rn(v.small, __shfl_xor_sync(0xffffffffu, v.small, d));
-  }
-  if (threadIdx.x % 32 == 0) slots[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = slots[0];
-#pragma unroll
-  for (int w = 1; w < 8; ++w) {
-    v.mid = __fadd_rn(v.mid, slots[w].mid);
-    v.big = __fadd_rn(v.big, slots[w].big);
-    v.small = __fadd_rn(v.small, slots[w].small);
-  }
-  return v;
-}
+using namespace orth;
 
 // Eight columns of a row, zeros past the last.
 template <int DT>
@@ -120,10 +93,7 @@ __global__ void __launch_bounds__(256) orth_start_kernel(const __grid_constant__
   for (int i = threadIdx.x; i < p.parts; i += 256)
     v.mid = __fadd_rn(v.mid, part[3 * i]), v.big = __fadd_rn(v.big, part[3 * i + 1]), v.small = __fadd_rn(v.small, part[3 * i + 2]);
   v = block_sum(v, slots);
-  const bool big = DT != kF16 && !(v.mid < 1e30f), small = DT != kF16 && v.mid < 1e-20f;
-  const float before = big ? kDown : small ? kUp : 1.f;
-  const float norm = __fadd_rn(__fsqrt_rn(big ? v.big : small ? v.small : v.mid), __fmul_rn(p.eps, before));
-  const float scale = __fdiv_rn(kHeldX, norm);
+  const Scale scale = scale_of(v, p.eps, DT);
   const T *g = static_cast<const T *>(p.g) + blockIdx.y * p.stride_g;
   __half *x = static_cast<__half *>(p.x[0]) + blockIdx.y * p.stride_x;
   const long long each = p.ld_x / 8, all = each * p.held_rows, step = gridDim.x * 256ll;
@@ -135,7 +105,7 @@ __global__ void __launch_bounds__(256) orth_start_kernel(const __grid_constant__
     for (int j = 0; j < 8; ++j) w[j] = 0.f;
     if (row < p.rows && c < p.cols) eight<DT>(p, g + row * p.ld_g, c, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(__fmul_rn(w[j], before), scale);
+    for (int j = 0; j < 8; ++j) w[j] = __fmul_rn(__fmul_rn(w[j], scale.before), scale.after);
     uint4 raw;
     narrow8<kF16>(w, &raw);
     *reinterpret_cast<uint4 *>(x + row * p.ld_x + c) = raw;
@@ -252,6 +222,7 @@ cudaError_t update(const OrthParams &p, const void *x, const gemm::Out &out, lon
 cudaError_t launch_orth(const OrthParams &p, cudaStream_t s) {
   using gemm::Operand;
   using gemm::Out;
+  if (orth_is_short(p.rows, p.cols)) return launch_orth_short(p, s);
   cudaError_t err = p.dtype == kF32 ? start<kF32>(p, s) : p.dtype == kF16 ? start<kF16>(p, s) : start<kBF16>(p, s);
   const bool tall = p.rows > p.cols;
   const long long m = tall ? p.held_cols : p.held_rows;

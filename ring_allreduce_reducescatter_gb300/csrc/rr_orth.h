@@ -14,7 +14,7 @@ struct OrthParams {
   void *out;
   long long rows, cols, ld_g, ld_out, stride_g, stride_out;  // strides: from matrix to matrix
   int batch, steps, dtype, out_dtype, parts;
-  bool vec;  // 16-byte groups of the rows of g are aligned
+  bool vec, vec_out;  // 16-byte groups of the rows of g, of out are aligned
   float eps;
   float *norms;       // [batch][parts][3]
   void *x[2], *s, *b; // binary16: two iterates, the Gram matrix and its polynomial
@@ -35,6 +35,9 @@ inline long long orth_held(long long n, long long rows, long long cols) {
   return rows * cols * 2 < (1 << 20) ? ceil_div(n, 128ll) * 128 : n;
 }
 
+// Matrices that one cluster holds, and their launch (rr_orth_short.cu).
+bool orth_is_short(long long rows, long long cols);
+cudaError_t launch_orth_short(const OrthParams &p, cudaStream_t s);
 cudaError_t launch_orth(const OrthParams &p, cudaStream_t s);
 
 }  // namespace rr

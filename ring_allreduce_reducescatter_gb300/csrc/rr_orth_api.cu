@@ -86,6 +86,7 @@ rr_status ring_orthogonalize(const void *g, size_t ld_g, size_t stride_g, rr_dty
   p.batch = (int)batch, p.steps = steps, p.dtype = dtype, p.out_dtype = out_dtype;
   p.eps = (float)eps;
   p.parts = rr::orth_parts(p.rows, p.cols);
+  p.vec_out = rr::aligned16(out, rows, ld_out, elem_bytes(out_dtype)) && (batch == 1 || stride_out * elem_bytes(out_dtype) % 16 == 0);
   p.vec = rr::aligned16(g, rows, ld_g, elem_bytes(dtype)) && (batch == 1 || stride_g * elem_bytes(dtype) % 16 == 0);
   p.norms = reinterpret_cast<float *>(ws + l.norms);
   p.x[0] = ws + l.x[0], p.x[1] = ws + l.x[1], p.s = ws + l.s, p.b = ws + l.b;

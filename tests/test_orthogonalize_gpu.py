@@ -50,7 +50,7 @@ def check(y, g, steps=5, eps=1e-7):
 
 
 SHAPES = [(1, 1), (1, 7), (9, 1), (2, 3), (16, 16), (32, 100), (100, 32), (127, 129), (128, 128), (128, 512), (640, 130),
-          (777, 1537), (1537, 777), (1000, 1000), (34, 4240), (2048, 2048), (1100, 2600), (2600, 1100), (4100, 260), (2300, 2400), (2400, 2310)]
+          (777, 1537), (1537, 777), (1000, 1000), (34, 4240), (128, 129), (100, 300), (640, 90), (128, 900), (33, 1024), (1025, 128), (77, 2048), (2040, 65), (64, 2049), (2048, 2048), (1100, 2600), (2600, 1100), (4100, 260), (2300, 2400), (2400, 2310)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
@@ -116,7 +116,7 @@ def test_zeros_and_no_numbers(rr):
 
 
 @pytest.mark.parametrize("pad,at", [(6, 0), (16, 16), (3, 1)])
-@pytest.mark.parametrize("rows,cols", [(60, 90), (90, 60), (300, 1000)])
+@pytest.mark.parametrize("rows,cols", [(60, 90), (90, 60), (300, 1000), (40, 1400), (700, 40)])
 def test_strides_guards_and_in_place(rr, rows, cols, pad, at):
     g = draw((2, rows, cols), 6, BF16)
     want = rr.orthogonalize(g)
@@ -132,7 +132,7 @@ def test_strides_guards_and_in_place(rr, rows, cols, pad, at):
 
 def test_nothing_past_the_workspace(rr):
     L = rr.lib()
-    for shape in ((1, 60, 90), (3, 777, 513)):
+    for shape in ((1, 60, 90), (3, 777, 513), (2, 128, 1500)):
         g = draw(shape, 7)
         want = rr.orthogonalize(g)
         need = L.ring_orthogonalize_workspace(*shape)

@@ -170,6 +170,10 @@ __device__ __forceinline__ void wait_turns(uint64_t *bars, unsigned end, unsigne
 //   chunk(c, v)    32 accumulators from column col + 32 c on (the whole warp
 //                  calls it; rows and columns past the product's are zero)
 //   end()          after the last chunk
+// kRun: steps of K after which the sums so far move to registers (0: none).  The
+// tensor cores cut a sum at every addition, always towards zero; a run's sums are
+// added up in binary32 rounded to nearest, while the next run's products go on in
+// the other accumulator.
 template <class S, int G, bool kMnA, bool kMnB, class Epi>
 __device__ __forceinline__ void product_body(const Product &p, const typename Epi::Params &e) {
   extern __shared__ unsigned char smem_raw[];
@@ -201,48 +205,66 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
     const int quarter = warp % 4, half = warp / 4;
     float *stage = reinterpret_cast<float *>(smem + S::kStages * S::kStageBytes) + warp * kStageFloats;
     unsigned i = 0;
-    for (long long t = worker; t < p.items; t += workers, ++i) {
+    bool ok = true;
+    unsigned steps = 0;
+    for (long long t = worker; t < p.items && ok; t += workers) {
       const Place w = place_of(p, t);
-      const unsigned buf = i & 1;
       const bool mine = G == 1 || w.whole || half == 0;  // a half tile is one half's warps' work
       Epi epi(e, (long long)w.tm * S::kBM + rank * 128 + quarter * 32 + lane,
               (long long)w.tn * S::kBN + (G == 1 || w.whole ? half : w.side) * S::kHalf, w.batch, stage);
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1, kWaitLimitNs))) {
-        if (lane == 0) atomicOr(p.status, kStatusWaitTimeout);
-        break;
-      }
-      tcgen05_fence_after();
-      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * S::kBN + half * S::kHalf;
       constexpr int kChunks = S::kHalf / kChunk;
-      const auto release = [&] {
-        tcgen05_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (G == 2) cluster_arrive_remote(cluster_addr(&acc_empty[buf], 0));
-          else asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&acc_empty[buf])) : "memory");
+      float total[Epi::kRun ? kChunks : 1][kChunk];
+      for (int k = 0; k < p.steps; k += Epi::kRun ? Epi::kRun : p.steps, ++i) {
+        const unsigned buf = i & 1;
+        const bool last = !Epi::kRun || k + Epi::kRun >= p.steps;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_full[buf], (i >> 1) & 1, kWaitLimitNs)))) {
+          if (lane == 0) atomicOr(p.status, kStatusWaitTimeout);
+          break;
         }
-      };
-      if (!mine) {
-        release();
-        continue;
-      }
-      uint32_t acc[2][kChunk];  // a chunk is on its way while the one before is worked on
-      tmem_load32(at, acc[0]);
+        tcgen05_fence_after();
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * S::kBN + half * S::kHalf;
+        const auto release = [&] {
+          tcgen05_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (G == 2) cluster_arrive_remote(cluster_addr(&acc_empty[buf], 0));
+            else asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&acc_empty[buf])) : "memory");
+          }
+        };
+        if (!mine) {
+          release();
+          continue;
+        }
+        uint32_t acc[2][kChunk];  // a chunk is on its way while the one before is worked on
+        tmem_load32(at, acc[0]);
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        tmem_loaded32(acc[c & 1]);
-        if (c + 1 < kChunks) tmem_load32(at + (c + 1) * kChunk, acc[(c + 1) & 1]);
-        else release();
-        float v[kChunk];
+        for (int c = 0; c < kChunks; ++c) {
+          tmem_loaded32(acc[c & 1]);
+          if (c + 1 < kChunks) tmem_load32(at + (c + 1) * kChunk, acc[(c + 1) & 1]);
+          else release();
+          if constexpr (Epi::kRun > 0) {
+            if (k == 0) {
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) v[j] = __uint_as_float(acc[c & 1][j]);
-        epi.chunk(c, v);
+              for (int j = 0; j < kChunk; ++j) total[c][j] = __uint_as_float(acc[c & 1][j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < kChunk; ++j) total[c][j] = __fadd_rn(total[c][j], __uint_as_float(acc[c & 1][j]));
+            }
+            if (last) epi.chunk(c, total[c]);
+          } else {
+            float v[kChunk];
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) v[j] = __uint_as_float(acc[c & 1][j]);
+            epi.chunk(c, v);
+          }
+        }
+        if (last) epi.end();
       }
-      epi.end();
+      if (ok) steps += (unsigned)p.steps;
     }
     // the commits of the last turns come before the CTA goes: one that came later
     // would meet another's barrier
-    if (warp == 0) wait_turns<S::kStages>(empty, i * (unsigned)p.steps, kLateLimitNs);
+    if (warp == 0) wait_turns<S::kStages>(empty, steps, kLateLimitNs);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) {
@@ -288,28 +310,31 @@ __device__ __forceinline__ void product_body(const Product &p, const typename Ep
       const bool one = elect_one();
       unsigned g = 0, i = 0;
       bool ok = true;
-      for (long long t = worker; t < p.items && ok; t += workers, ++i) {
-        const unsigned buf = i & 1;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty[buf], ((i >> 1) & 1) ^ 1, kWaitLimitNs)))) break;
-        tcgen05_fence_after();
-        const uint32_t d = tmem + buf * S::kBN;
+      for (long long t = worker; t < p.items && ok; t += workers) {
         const uint32_t idesc = G == 1 || t < p.whole ? instr_desc(p.format, kMnA, kMnB, S::kBM, S::kBN)
                                                      : instr_desc(p.format, kMnA, kMnB, S::kBM, S::kBN / 2);
-        for (int k = 0; k < p.steps; ++k, ++g) {
-          const unsigned s = g % S::kStages;
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (g / S::kStages) & 1, kWaitLimitNs)))) break;
+        for (int from = 0; from < p.steps && ok; from += Epi::kRun ? Epi::kRun : p.steps, ++i) {
+          const unsigned buf = i & 1;
+          const int end = Epi::kRun && from + Epi::kRun < p.steps ? from + Epi::kRun : p.steps;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&acc_empty[buf], ((i >> 1) & 1) ^ 1, kWaitLimitNs)))) break;
           tcgen05_fence_after();
-          const uint32_t a = smem_addr(smem) + s * S::kStageBytes, b = a + S::kBytesA;
-          if (one) {
+          const uint32_t d = tmem + buf * S::kBN;
+          for (int k = from; k < end; ++k, ++g) {
+            const unsigned s = g % S::kStages;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait_bounded(&full[s], (g / S::kStages) & 1, kWaitLimitNs)))) break;
+            tcgen05_fence_after();
+            const uint32_t a = smem_addr(smem) + s * S::kStageBytes, b = a + S::kBytesA;
+            if (one) {
 #pragma unroll
-            for (int j = 0; j < kStep / 16; ++j)
-              mma<G>(d, kMnA ? rows_desc(a + 2048 * j) : operand_desc(a + 32 * j),
-                     kMnB ? rows_desc(b + 2048 * j) : operand_desc(b + 32 * j), idesc, k > 0 || j > 0);
-            tcgen05_commit<G>(&empty[s]);
+              for (int j = 0; j < kStep / 16; ++j)
+                mma<G>(d, kMnA ? rows_desc(a + 2048 * j) : operand_desc(a + 32 * j),
+                       kMnB ? rows_desc(b + 2048 * j) : operand_desc(b + 32 * j), idesc, k > from || j > 0);
+              tcgen05_commit<G>(&empty[s]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          if (ok && one) tcgen05_commit<G>(&acc_full[buf]);  // a tile that was given up is not stored
         }
-        if (ok && one) tcgen05_commit<G>(&acc_full[buf]);  // a tile that was given up is not stored
       }
       if (!ok) {
         if (one) atomicOr(p.status, kStatusWaitTimeout);

@@ -27,6 +27,7 @@ __device__ __forceinline__ float exp_above(float a, float b) {
 }
 
 struct Statistics {
+  static constexpr int kRun = 8;  // 512 elements of K (whole, a loss of 8 was off by 1e-5 at 4096)
   struct Params {
     const long long *target;
     float2 *parts;

@@ -28,6 +28,7 @@ __device__ __forceinline__ float ex2(float x) {
 
 template <int DT>
 struct LogitGradient {
+  static constexpr int kRun = 0;
   struct Params {
     const long long *target;
     const float *lse;
@@ -72,6 +73,7 @@ struct LogitGradient {
 // D times the factors' power of two to storage.
 template <int DT>
 struct Scaled {
+  static constexpr int kRun = 0;
   struct Params {
     gemm::Out out;
     const float *scale;
@@ -93,6 +95,7 @@ struct Scaled {
 // The sum over pieces: D onto the pieces before it, to storage with the last.
 template <int DT>
 struct Summed {
+  static constexpr int kRun = 0;
   struct Params {
     gemm::Out out;
     const float *scale;

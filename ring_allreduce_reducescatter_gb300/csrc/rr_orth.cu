@@ -115,6 +115,7 @@ __global__ void __launch_bounds__(256) orth_start_kernel(const __grid_constant__
 // alpha D + beta C to storage; of a symmetric D also its mirror image.
 template <int DT>
 struct Combined {
+  static constexpr int kRun = 0;
   struct Params {
     gemm::Out out;
     long long out_stride;

@@ -72,18 +72,19 @@ def _rows(t, name: str):
 # ------------------------------------------------------------------ layer norm
 
 
-def _weights(x, cols, dtype, **named):
-    """The C code of the weights' one dtype (x's where there are none)."""
+def _weights(x, cols, code, weight, bias):
+    """The C code of the weights' one dtype (x's, ``code``, where there are none)."""
     wtype = None
-    for name, t in named.items():
+    for name, t in (("weight", weight), ("bias", bias)):
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or tuple(t.shape) != (cols,) or not t.is_contiguous() or t.device != x.device:
+        if not isinstance(t, torch.Tensor) or t.shape != (cols,) or not t.is_contiguous() or t.device != x.device:
             raise ValueError(f"{name}: needs a contiguous tensor of {cols} elements on {x.device}")
-        if t.dtype not in (x.dtype, _F32) or (wtype is not None and t.dtype != wtype):
-            raise ValueError(f"{name}: {t.dtype}; the weights have one dtype, x's ({x.dtype}) or float32")
-        wtype = t.dtype
-    return dtype if wtype is None else _dtype(wtype)
+        got = t.dtype
+        if (got != x.dtype and got != _F32) or (wtype is not None and got != wtype):
+            raise ValueError(f"{name}: {got}; the weights have one dtype, x's ({x.dtype}) or float32")
+        wtype = got
+    return code if wtype is None or wtype == x.dtype else 0
 
 
 def _at(t):
@@ -106,18 +107,17 @@ def layer_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None, b
 def _norm(x, weight, bias, eps, out, stats):
     rows, cols, ld = _rows(x, "x")
     code, device, handle = _dtype(x.dtype), x.device, _current(x.device)
-    wcode = _weights(x, cols, code, weight=weight, bias=bias)
+    wcode = _weights(x, cols, code, weight, bias)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
-        ld_out = cols
+        out, ld_out = torch.empty(x.shape, dtype=x.dtype, device=device), cols
     else:
         _, _, ld_out = _rows(out, "out")
         if out.shape != x.shape or out.dtype != x.dtype or out.device != device:
             raise ValueError("x and out must have one shape, dtype and device")
     mean = rstd = None
     if stats:
-        both = torch.empty((2,) + tuple(x.shape[:-1]), dtype=_F32, device=device)
-        mean, rstd = both[0], both[1]
+        mean = torch.empty(x.shape[:-1], dtype=_F32, device=device)
+        rstd = torch.empty_like(mean)
     status = (_L or _lib()).ring_layer_norm(x.data_ptr(), ld, _at(weight), _at(bias), wcode, eps, out.data_ptr(), ld_out,
                                             _at(mean), _at(rstd), rows, cols, code, handle)
     if status:
@@ -137,19 +137,21 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, r
     device = x.device
     if dy.shape != x.shape or dy.dtype != x.dtype or dy.device != device:
         raise ValueError("x and dy must have one shape, dtype and device")
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if (not isinstance(t, torch.Tensor) or t.dtype != _F32 or t.shape != x.shape[:-1] or t.device != device
+    for t in (mean, rstd):
+        if (not isinstance(t, torch.Tensor) or t.dtype != _F32 or t.numel() != rows or t.device != device
                 or not t.is_contiguous()):
-            raise ValueError(f"{name}: needs a contiguous float32 tensor of shape {tuple(x.shape[:-1])} on {device}")
+            raise ValueError(f"mean and rstd: need contiguous float32 tensors of {rows} elements on {device}")
     code, handle = _dtype(x.dtype), _current(device)
-    wcode = _weights(x, cols, code, weight=weight)
-    wtype = weight.dtype if weight is not None else x.dtype if wdtype is None else wdtype
-    if wtype not in (x.dtype, _F32):
-        raise ValueError(f"wdtype {wtype}: x's dtype ({x.dtype}) or float32 is wanted")
-    wcode = _dtype(wtype)
+    wcode, wtype = _weights(x, cols, code, weight, None), x.dtype
+    if weight is not None:
+        wtype = weight.dtype
+    elif wdtype is not None and wdtype != wtype:
+        if wdtype != _F32:
+            raise ValueError(f"wdtype {wdtype}: x's dtype ({x.dtype}) or float32 is wanted")
+        wtype, wcode = _F32, 0
     dx = torch.empty(x.shape, dtype=x.dtype, device=device) if want_dx else None
     dweight = torch.empty(cols, dtype=wtype, device=device) if want_dweight else None
-    dbias = torch.empty(cols, dtype=wtype, device=device) if want_dbias else None
+    dbias = None if not want_dbias else torch.empty_like(dweight) if want_dweight else torch.empty(cols, dtype=wtype, device=device)
     L = _L or _lib()
     need = L.ring_layer_norm_workspace(rows, cols) if want_dweight or want_dbias else 0
     space = torch.empty(need, dtype=torch.uint8, device=device) if need else None
@@ -205,7 +207,7 @@ def _loss_operands(x, w, target):
         raise ValueError(f"x has {hidden} columns, w {h}")
     if x.dtype != w.dtype or x.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError(f"x is {x.dtype}, w {w.dtype}: both float16 or both bfloat16 are wanted")
-    if (not isinstance(target, torch.Tensor) or target.dtype != torch.int64 or tuple(target.shape) != (tokens,)
+    if (not isinstance(target, torch.Tensor) or target.dtype != torch.int64 or target.shape != (tokens,)
             or not target.is_contiguous()):
         raise ValueError(f"target: needs a contiguous int64 tensor of {tokens} elements")
     if w.device != x.device or target.device != x.device:
@@ -220,7 +222,7 @@ def _losses(x, w, target, ignore_index, want_lse, want_sums):
     tokens, hidden, vocabulary, ld_x, ld_w, code = _loss_operands(x, w, target)
     device, handle, L = x.device, _current(x.device), _L or _lib()
     loss = torch.empty(tokens, dtype=_F32, device=device)
-    lse = torch.empty(tokens, dtype=_F32, device=device) if want_lse else None
+    lse = torch.empty_like(loss) if want_lse else None
     sums = torch.empty(3, dtype=_F32, device=device) if want_sums else None
     at = (x.data_ptr(), ld_x, w.data_ptr(), ld_w)
     need = L.ring_linear_cross_entropy_workspace(*at, tokens, hidden, vocabulary)
@@ -255,9 +257,9 @@ def linear_cross_entropy_backward(grad: torch.Tensor, x: torch.Tensor, w: torch.
     tokens, hidden, vocabulary, ld_x, ld_w, code = _loss_operands(x, w, target)
     device = x.device
     if (not isinstance(grad, torch.Tensor) or grad.dtype != _F32 or grad.device != device or not grad.is_contiguous()
-            or not (grad.numel() == 1 or tuple(grad.shape) == (tokens,))):
+            or not (grad.numel() == 1 or grad.shape == (tokens,))):
         raise ValueError(f"grad: needs a contiguous float32 tensor of one element or of {tokens} on {device}")
-    if (not isinstance(lse, torch.Tensor) or lse.dtype != _F32 or lse.device != device or tuple(lse.shape) != (tokens,)
+    if (not isinstance(lse, torch.Tensor) or lse.dtype != _F32 or lse.device != device or lse.shape != (tokens,)
             or not lse.is_contiguous()):
         raise ValueError(f"lse: needs a contiguous float32 tensor of {tokens} elements on {device}")
     handle, L = _current(device), _L or _lib()

@@ -175,10 +175,11 @@ __global__ void __launch_bounds__(1024) loss_factors_kernel(const __grid_constan
 
 // A copy in rows of ld_to, for operands that tensor copies do not read as they lie:
 // eight elements a thread, put together from the aligned 16-byte groups around them
-// where those lie inside the matrix.
-__global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ PadParams p) {
+// where those lie inside the matrix.  blockIdx.y: which of the copies.
+__global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ PadParams both) {
   grid_dependency_wait();
   grid_dependents_launch();
+  const Pad &p = both.copy[blockIdx.y];
   const uint16_t *from = static_cast<const uint16_t *>(p.from);
   uint16_t *to = static_cast<uint16_t *>(p.to);
   const uintptr_t lo = reinterpret_cast<uintptr_t>(from), hi = lo + (uintptr_t)(((p.rows - 1) * p.ld_from + p.cols) * 2);
@@ -207,9 +208,9 @@ __global__ void __launch_bounds__(256) pad_kernel(const __grid_constant__ PadPar
 }
 
 template <class... P, class... Args>
-cudaError_t launch(void (*k)(P...), long long grid, int block, cudaStream_t s, const Args &...args) {
+cudaError_t launch(void (*k)(P...), dim3 grid, int block, cudaStream_t s, const Args &...args) {
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)grid);
+  c.gridDim = grid;
   c.blockDim = dim3((unsigned)block);
   c.stream = s;
   cudaLaunchAttribute a = {};
@@ -223,13 +224,17 @@ cudaError_t launch(void (*k)(P...), long long grid, int block, cudaStream_t s, c
 }  // namespace
 
 cudaError_t launch_pad(const PadParams &p, cudaStream_t s) {
-  const long long groups = ceil_div(p.rows_to * (p.ld_to / 8), 256ll);
-  return launch(pad_kernel, groups < 2048 ? groups : 2048, 256, s, p);
+  long long groups = 0;
+  for (int i = 0; i < p.n; ++i) {
+    const long long each = ceil_div(p.copy[i].rows_to * (p.copy[i].ld_to / 8), 256ll);
+    groups = groups > each ? groups : each;
+  }
+  return launch(pad_kernel, dim3((unsigned)(groups < 2048 ? groups : 2048), (unsigned)p.n), 256, s, p);
 }
 
 cudaError_t launch_loss(const LossParams &p, cudaStream_t s) {
   const long long tokens = p.x.rows, vocabulary = p.w.rows, group = loss_group(tokens), groups = ceil_div(vocabulary, group);
-  if (tokens == 0) return launch(loss_sums_kernel, 1, 1024, s, p);
+  if (tokens == 0) return launch(loss_sums_kernel, dim3(1), 1024, s, p);
   const gemm::Operand a{p.x.at, p.x.padded, p.hidden, p.x.ld, 0, 1, false}, b{p.w.at, vocabulary, p.hidden, p.w.ld, 0, 1, false};
   const Statistics::Params e{p.target, p.parts, p.chosen, tokens, vocabulary, group};
   // (groups of columns go by the tiles' width: the tokens alone choose)
@@ -241,14 +246,14 @@ cudaError_t launch_loss(const LossParams &p, cudaStream_t s) {
                                a, b, false, format, p.status, p.sms, e, s);
   if (err != cudaSuccess) return err;
   // few rows: a CTA on each (one token of 131072 has 2048 groups)
-  err = tokens <= 4 * p.sms ? launch(loss_rows_kernel<1>, tokens, 256, s, p, groups)
-                            : launch(loss_rows_kernel<8>, ceil_div(tokens, 8ll), 256, s, p, groups);
+  err = tokens <= 4 * p.sms ? launch(loss_rows_kernel<1>, dim3((unsigned)tokens), 256, s, p, groups)
+                            : launch(loss_rows_kernel<8>, dim3((unsigned)ceil_div(tokens, 8ll)), 256, s, p, groups);
   if (err != cudaSuccess || !p.sums) return err;
-  return launch(loss_sums_kernel, 1, 1024, s, p);
+  return launch(loss_sums_kernel, dim3(1), 1024, s, p);
 }
 
 cudaError_t launch_loss_factors(const LossGradParams &p, cudaStream_t s) {
-  return launch(loss_factors_kernel, 1, 1024, s, p);
+  return launch(loss_factors_kernel, dim3(1), 1024, s, p);
 }
 
 }  // namespace rr

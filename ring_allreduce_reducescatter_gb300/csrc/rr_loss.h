@@ -46,11 +46,15 @@ struct LossGradParams {
   int dtype, sms;
 };
 
-struct PadParams {
+struct Pad {
   const void *from;
   void *to;
   long long rows, cols, ld_from, ld_to;  // 16-bit elements
   long long rows_to;  // zeros behind the rows, and behind the columns up to ld_to
+};
+struct PadParams {
+  Pad copy[2];
+  int n;
 };
 
 constexpr float kLossWiden = 16384.f;  // what the logits' gradient is held times in binary16

@@ -78,15 +78,13 @@ rr_status place(const Operands &o, char *ws, const void *x, size_t ld_x, const v
   *mx = rr::LossMatrix{o.copy_x ? ws + o.x_at : x, (long long)tokens, (long long)o.rows, (long long)(o.copy_x ? o.ld : ld_x)};
   *mw = rr::LossMatrix{o.copy_w ? ws + o.w_at : w, (long long)vocabulary, (long long)vocabulary,
                        (long long)(o.copy_w ? o.ld : ld_w)};
-  if (o.copy_x) {
-    const rr::PadParams p{x, ws + o.x_at, (long long)tokens, (long long)hidden, (long long)ld_x, (long long)o.ld, (long long)o.rows};
-    if (!rr::note_cuda(rr::launch_pad(p, stream))) return RR_ERR_CUDA;
-  }
-  if (o.copy_w) {
-    const rr::PadParams p{w, ws + o.w_at, (long long)vocabulary, (long long)hidden, (long long)ld_w, (long long)o.ld,
-                          (long long)vocabulary};
-    if (!rr::note_cuda(rr::launch_pad(p, stream))) return RR_ERR_CUDA;
-  }
+  rr::PadParams p{};
+  if (o.copy_x)
+    p.copy[p.n++] = rr::Pad{x, ws + o.x_at, (long long)tokens, (long long)hidden, (long long)ld_x, (long long)o.ld, (long long)o.rows};
+  if (o.copy_w)
+    p.copy[p.n++] = rr::Pad{w, ws + o.w_at, (long long)vocabulary, (long long)hidden, (long long)ld_w, (long long)o.ld,
+                            (long long)vocabulary};
+  if (p.n > 0 && !rr::note_cuda(rr::launch_pad(p, stream))) return RR_ERR_CUDA;
   return RR_OK;
 }
 

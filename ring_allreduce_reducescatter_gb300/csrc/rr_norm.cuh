@@ -531,7 +531,10 @@ struct Walk {
 // columns throughout, and with them their weights (as stored, where they fit) and
 // their part of dweight and dbias in registers: the sums over rows cost one write of
 // two rows a CTA, and the rest is norm_sums_kernel's.  Rows go to CTAs by their
-// index, so the order of the sums does not depend on timing.
+// index, so the order of the sums does not depend on timing.  16384 x 4096 takes 79
+// us (and 7 for the sums) in bfloat16, 126 in binary32, 0.75 and 0.94 of the copy
+// rate: twelve working warps an SM leave half the issue slots empty, but threads
+// with half the columns and twice the warps took 93.
 template <int DT, int WT, bool kVec, int kRow, int kNv>
 __global__ void __launch_bounds__(Ring<kRow, kNv, 2>::kAll, Ring<kRow, kNv, 2>::kCtas)
     norm_grad_ring_kernel(const __grid_constant__ NormGradParams p) {

@@ -270,6 +270,40 @@ def test_parts_and_no_tokens(rr):
     assert dx.shape == (0, 64) and (dw == 0).all() and dw.shape == w.shape
 
 
+def test_past_four_billion_elements(rr):
+    """Rows of w and dw beyond element 2^32: all rows but the first and last thousand are zero, their logits 0."""
+    tokens, hidden, vocabulary, k = 130, 4096, (1 << 20) + 5000, 1000
+    w = torch.zeros((vocabulary, hidden), dtype=BF16, device="cuda")
+    w[:k], w[-k:] = draw((k, hidden), 1, BF16, 0.05), draw((k, hidden), 2, BF16, 0.05)
+    x = draw((tokens, hidden), 3, BF16)
+    target = torch.randint(0, vocabulary, (tokens,), generator=torch.Generator(device="cuda").manual_seed(4), device="cuda")
+    target[::2] = vocabulary - 1 - torch.arange(65, device="cuda") * 7
+    ends = torch.cat((w[:k], w[-k:]))
+    l = x.double() @ ends.double().t()
+    lse = (l.exp().sum(1) + (vocabulary - 2 * k)).log()
+    at = torch.where(target < k, target, target - vocabulary + 2 * k)  # in `ends`, where it is there
+    there = (target < k) | (target >= vocabulary - k)
+    chosen = torch.where(there, l.gather(1, at.clamp(0, 2 * k - 1)[:, None]).squeeze(1), 0.0)
+    loss, got = rr.linear_cross_entropy_forward(x, w, target)
+    d, off = lse_error(x, ends, lse)
+    off = off + (vocabulary // 64) * U
+    assert ((got.double() - lse).abs() <= off).all()
+    assert ((loss.double() - (lse - chosen)).abs() <= 2 * off + d).all()
+    dx, dw = rr.linear_cross_entropy_backward(torch.ones((), device="cuda"), x, w, target, got)
+    e = torch.exp(l - lse[:, None])
+    rows = torch.arange(tokens, device="cuda")[there]
+    e[rows, at[there]] -= 1
+    want = e.t() @ x.double()
+    for part, here in ((dw[:k], want[:k]), (dw[-k:], want[-k:])):
+        assert (part.double() - here).norm() <= 2 * ref.half_step(BF16) * here.norm()
+    assert (dx.double() - e @ ends.double()).norm() <= 2 * ref.half_step(BF16) * (e @ ends.double()).norm()
+    middle = int(target[~there][0])
+    one = (e.new_zeros(hidden) + (torch.exp(-lse)[:, None] * x.double()).sum(0)) - x[target == middle].double().sum(0)
+    assert (dw[middle].double() - one).norm() <= 2 * ref.half_step(BF16) * one.norm()
+    del w, dw
+    torch.cuda.empty_cache()
+
+
 def test_same_bits_every_time(rr):
     x, w, target = inputs(1000, 200, 3000, BF16)
     loss, lse = rr.linear_cross_entropy_forward(x, w, target)

@@ -144,6 +144,20 @@ def test_nothing_past_the_workspace(rr):
         assert st == 0 and torch.equal(out, want) and (space[need:] == 0xFF).all()
 
 
+def test_past_four_billion_elements(rr):
+    """Matrices of a batch beyond element 2^32 of g, of the iterates and of the output."""
+    batch, n = 260, 4096
+    g = torch.empty((batch, n, n), dtype=BF16, device="cuda")
+    for k in range(batch):
+        g[k] = draw((n, n), 12 + k % 3, BF16)
+    y = rr.orthogonalize(g, steps=2)
+    for k in (0, batch - 1):
+        check(y[k], g[k], 2)
+    assert torch.equal(y[batch - 3], y[batch - 6])  # (the same matrix)
+    del g, y
+    torch.cuda.empty_cache()
+
+
 def test_same_bits_every_time(rr):
     g = draw((1100, 1300), 8, BF16)
     first = rr.orthogonalize(g)
